@@ -463,6 +463,161 @@ kvq_status kvq_decode_attention_paged(const kvq_format* fmt, const kvq_paged_cac
                                       void* out, int32_t out_dtype, void* workspace,
                                       size_t workspace_bytes, int32_t* d_status, void* stream);
 
+/* ---- Serving steps around the paged cache ----------------------------------------
+ * The pages describe the cache and the decode over it.  A server also has to bring each
+ * step's tokens into the cache and let several of them attend at once; the entry points
+ * below do that, in the order a step uses them: kvq_norm_rope (queries, keys),
+ * kvq_append_paged, then kvq_attention_paged (several new tokens per sequence) or
+ * kvq_decode_attention_paged (one).  kvq_read_paged hands tokens back out of the pages.
+ *
+ * Ragged batches.  A batch of num_seqs sequences is given as rows back to back, the rows
+ * of sequence s being [cu[s], cu[s + 1]) of the row arrays: cu is device int32
+ * [num_seqs + 1], ascending, cu[0] >= 0 and cu[num_seqs] <= n_rows, the rows the arrays
+ * hold.  Rows outside every sequence are left alone.  An empty sequence is allowed.
+ *
+ * Lengths.  A sequence holds n_sink + t_quant[s] + t_res[s] tokens in position order:
+ * its sink rows, packed tokens [0, t_quant[s]) and window rows [0, t_res[s]).  While the
+ * sink itself still fills, t_quant[s] is 0 and t_res[s] lies in [-n_sink, 0): the sum is
+ * the number of sink rows in use, and a new sequence has t_res = -n_sink.  (The decode
+ * call takes full sinks only.)  A sequence whose device-side numbers are out of range
+ * raises KVQ_DEV_BOUNDS, and its work is skipped as stated at each call. */
+
+/* Rotary frequencies and their scaling for contexts longer than `original_len` positions.
+ * With w_i = base^(-2i/R), i = 0 .. R/2 - 1, R = rot_dim:
+ *   PLAIN   f_i = w_i
+ *   LINEAR  f_i = w_i / factor
+ *   BANDS   by turns t_i = original_len * w_i / (2 pi) within the original context:
+ *           g_i = clamp((t_i - low) / (high - low), 0, 1),
+ *           f_i = (1 - g_i) w_i / factor + g_i w_i
+ *   RAMP    by index: x(b) = R ln(original_len / (2 pi b)) / (2 ln base),
+ *           a = max(floor(x(high)), 0), z = min(ceil(x(low)), R - 1),
+ *           g_i = clamp((i - a) / max(z - a, 0.001), 0, 1),
+ *           f_i = (1 - g_i) w_i + g_i w_i / factor
+ * `amplitude` multiplies cosine and sine (1 for none).  All of it in double. */
+enum { KVQ_ROPE_PLAIN = 0, KVQ_ROPE_LINEAR = 1, KVQ_ROPE_BANDS = 2, KVQ_ROPE_RAMP = 3 };
+typedef struct kvq_rope_spec {
+  int32_t rot_dim;       /* R: channels that turn, a multiple of 16 in [16, 256]          */
+  int32_t scaling;
+  double base;           /* > 1                                                           */
+  double factor;         /* > 0 (LINEAR, BANDS, RAMP)                                     */
+  double original_len;   /* > 0 (BANDS, RAMP)                                             */
+  double low, high;      /* 0 < low < high (BANDS, RAMP)                                  */
+  double amplitude;      /* finite, > 0                                                   */
+} kvq_rope_spec;
+
+/* The rotary table of positions [pos0, pos0 + n_pos): row p of `table` (device fp32
+ * [n_pos][rot_dim], 16-byte aligned) holds amplitude * cos((pos0 + p) f_i) for every pair i,
+ * then amplitude * sin((pos0 + p) f_i), each evaluated in double and rounded once.
+ * pos0 >= 0, n_pos >= 0, pos0 + n_pos <= 2^31. */
+kvq_status kvq_rope_table(const kvq_rope_spec* spec, int64_t pos0, int64_t n_pos, float* table,
+                          void* stream);
+
+/* A rotation by such a table (its row 0 = position 0).  Of each head the first rot_dim
+ * channels turn, the rest stay: pairs (i, i + rot_dim / 2), or (2i, 2i + 1) when
+ * interleaved, i < rot_dim / 2, become (x1 c - x2 s, x2 c + x1 s) with every product and
+ * sum rounded to fp32. */
+typedef struct kvq_rope {
+  const float* table;    /* device fp32 [n_pos][rot_dim], 16-byte aligned                 */
+  int64_t n_pos;
+  int32_t rot_dim;       /* a multiple of 16, at most the head dimension                  */
+  int32_t interleaved;
+} kvq_rope;
+
+/* One set of heads of kvq_norm_rope: row t of head h starts at element
+ * t * stride_t + h * stride_h of `x`, likewise of `y`; every stride * element size is a
+ * multiple of 16 bytes.  y may be x (with the same strides), otherwise the two must not
+ * overlap.  `weight`: device [head_dim] in the rows' dtype, 16-byte aligned, or NULL for no
+ * norm. */
+typedef struct kvq_head_rows {
+  const void* x;
+  void* y;
+  int64_t x_stride_t, x_stride_h, y_stride_t, y_stride_h;
+  int32_t heads;
+  const void* weight;
+} kvq_head_rows;
+
+/* Norm of each query and key head and the rotation of their positions, in one pass: for
+ * every row x of head_dim channels (a multiple of 16 in [16, 256]; fp32, fp16 or bf16)
+ *   u = x / sqrt(mean(x^2) + eps) * (weight_offset + weight)      (u = x without a weight)
+ *   y = u turned by the table's row of the token's position
+ * in fp32, rounded once to `dtype`.  `k` may be NULL (queries only).  rope may be NULL (norm
+ * only).  positions: device int32 [n_tokens], NULL for position = token index; a position
+ * outside [0, n_pos) leaves the row unturned and raises KVQ_DEV_BOUNDS. */
+kvq_status kvq_norm_rope(int32_t head_dim, int32_t dtype, int64_t n_tokens, const kvq_head_rows* q,
+                         const kvq_head_rows* k, float eps, float weight_offset, const kvq_rope* rope,
+                         const int32_t* positions, int32_t* d_status, void* stream);
+
+/* Append new tokens to every sequence of a paged cache.  Rows [cu_new[s], cu_new[s + 1])
+ * of k_src / v_src (src_dtype, [row][kv head][D] at row * stride_t + h * stride_h, one pair
+ * of strides for each) follow the tokens sequence s holds, at positions n_sink + t_quant[s]
+ * + t_res[s], ...: first into the sink while it has room, then into the raw window.  When
+ * the window's rows and the new ones together reach residual_cap (a positive multiple of
+ * group_tokens here), every whole group among them is packed into pages, the oldest tokens
+ * first, group j into block block_table[s][t_quant[s] / group_tokens + j], and the rest
+ * (fewer than group_tokens, new tokens all) become window rows [0, ...): the flush of the
+ * full recent window of [MIX] Figure 4.  t_quant_out / t_res_out (device int32
+ * [num_seqs], distinct from the inputs) receive the lengths after it.
+ * rope (nullable) turns the new keys on the way at their positions, or at positions[row]
+ * when `positions` (device int32 [n_rows]) is given; the turned key is rounded to
+ * src_dtype before it is stored or packed, so a token is packed from the same bits whether
+ * or not it passed through the window.  Packed groups equal kvq_quantize_kv_paged's.
+ * max_new: host bound on the new tokens of one sequence.  A sequence is left as it was, its
+ * lengths copied and KVQ_DEV_BOUNDS raised, when its rows or lengths are out of range, it
+ * brings more than max_new tokens, t_quant[s] is not a multiple of group_tokens, or a block
+ * it needs is missing from the table or outside the pool.  A position outside the rotary
+ * table leaves that key unturned and raises KVQ_DEV_BOUNDS.  Formats: those of the paged
+ * cache above.  Two sequences must not share a block that is written. */
+kvq_status kvq_append_paged(const kvq_format* fmt, const kvq_paged_cache* cache, const int32_t* cu_new,
+                            int64_t n_rows, int64_t max_new, const int32_t* t_quant, const int32_t* t_res,
+                            const void* k_src, int64_t k_stride_t, int64_t k_stride_h, const void* v_src,
+                            int64_t v_stride_t, int64_t v_stride_h, const kvq_rope* rope,
+                            const int32_t* positions, int32_t* t_quant_out, int32_t* t_res_out,
+                            int32_t* d_status, void* stream);
+
+/* Read cached tokens back as rows: for sequence s the tokens at positions first[s],
+ * first[s] + 1, ... (device int32 [num_seqs]), as many as the rows [cu[s], cu[s + 1]), into
+ * k_out / v_out (device [n_rows][kv_heads][D] contiguous, out_dtype; either may be NULL).
+ * Packed tokens are the x^ of the scheme as kvq_dequantize gives it, raw ones the stored
+ * value; both rounded to out_dtype.  max_rows: host bound on the rows of one sequence.
+ * Rows of a sequence whose numbers are out of range, or that asks for a token it does not
+ * hold, are left alone and raise KVQ_DEV_BOUNDS; so does a page missing from the table
+ * (its rows are left alone).  Formats: those of the paged cache above. */
+kvq_status kvq_read_paged(const kvq_format* fmt, const kvq_paged_cache* cache, const int32_t* cu,
+                          int64_t n_rows, int64_t max_rows, const int32_t* first, const int32_t* t_quant,
+                          const int32_t* t_res, void* k_out, void* v_out, int32_t out_dtype,
+                          int32_t* d_status, void* stream);
+
+/* Workspace bytes for kvq_attention_paged with these sizes (depends on the current
+ * device's SM count); 0 for sizes it refuses. */
+size_t kvq_attention_paged_workspace_bytes(const kvq_format* fmt, int32_t num_seqs, int32_t q_heads,
+                                           int32_t kv_heads, int64_t n_rows, int64_t max_new,
+                                           int64_t max_t_quant, int32_t max_t_res);
+
+/* Attention of several new tokens per sequence over a paged cache that already holds them
+ * (kvq_append_paged first).  Query rows [cu_q[s], cu_q[s + 1]) of q ([n_rows][q_heads][D]
+ * contiguous, q_dtype) are the last n tokens of sequence s, which holds L = n_sink +
+ * t_quant[s] + t_res[s] tokens; row i attends to the tokens at positions j <= L - n + i
+ * when causal, to all L otherwise:
+ *   out[i][h] = sum_j softmax_j(softmax_scale * q[i][h] . k^_j) v^_j
+ * out: device [n_rows][q_heads][D] in out_dtype; lse (device fp32 [n_rows][q_heads], may
+ * be NULL): the natural log of the softmax denominator, as kvq_merge_states takes it.  A row
+ * that sees no token (n > L) gets out = 0 and lse = -inf.  The products run on the tensor
+ * cores with fp16 operands and fp32 sums: queries (scaled by a power of two of their own
+ * row), probabilities and reconstructed or raw keys and values are each rounded to fp16
+ * once.  A raw key or value beyond fp16's range raises KVQ_DEV_RANGE, a NaN or Inf one
+ * KVQ_DEV_NONFINITE; either counts as 0 there, so rows that do not see it are unaffected.
+ * max_new, max_t_quant, max_t_res: host bounds as in the calls above.  A sequence whose
+ * numbers are out of range (t_quant above max_t_quant and the like) keeps its rows as they
+ * were and raises KVQ_DEV_BOUNDS; a page missing from the table or outside the pool raises
+ * it too and its tokens are read from block 0.  Formats: those of the paged cache above
+ * (D = 128, group_tokens 128), q_heads / kv_heads <= 16. */
+kvq_status kvq_attention_paged(const kvq_format* fmt, const kvq_paged_cache* cache, const int32_t* cu_q,
+                               int64_t n_rows, int64_t max_new, const int32_t* t_quant,
+                               const int32_t* t_res, int64_t max_t_quant, int32_t max_t_res,
+                               const void* q, int32_t q_dtype, int32_t q_heads, float softmax_scale,
+                               int32_t causal, void* out, int32_t out_dtype, float* lse, void* workspace,
+                               size_t workspace_bytes, int32_t* d_status, void* stream);
+
 /* Decode attention without a caller workspace, for callers that cannot allocate
  * device memory at all -- for example a serving process whose allocator reserved
  * every byte at start-up, or a plugin host that forbids allocation once running --

@@ -316,6 +316,17 @@ kvq_status make_layout(const kvq_format* f, const kvq_cache* c, Layout* L) {
   return KVQ_OK;
 }
 
+kvq_status paged_layout(const kvq_format* f, const kvq_paged_cache* pc, Layout* L) {
+  if (!pc) return KVQ_ERR_INVALID;
+  kvq_status st = make_layout(f, &pc->pool, L);
+  if (st != KVQ_OK) return st;
+  if (pc->pool.capacity != f->group_tokens) return KVQ_ERR_INVALID;
+  if (pc->num_seqs < 1 || pc->max_blocks < 1 || !pc->block_table ||
+      (reinterpret_cast<uintptr_t>(pc->block_table) & 3))
+    return KVQ_ERR_INVALID;
+  return KVQ_OK;
+}
+
 int device_sm_count() {
   int dev = 0, n = 148;
   if (cudaGetDevice(&dev) != cudaSuccess) return 148;
@@ -641,17 +652,6 @@ kvq_status kvq_decode_attention(const kvq_format* f, const kvq_cache* c, const v
   return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
-
-static kvq_status paged_layout(const kvq_format* f, const kvq_paged_cache* pc, Layout* L) {
-  if (!pc) return KVQ_ERR_INVALID;
-  kvq_status st = make_layout(f, &pc->pool, L);
-  if (st != KVQ_OK) return st;
-  if (pc->pool.capacity != f->group_tokens) return KVQ_ERR_INVALID;
-  if (pc->num_seqs < 1 || pc->max_blocks < 1 || !pc->block_table ||
-      (reinterpret_cast<uintptr_t>(pc->block_table) & 3))
-    return KVQ_ERR_INVALID;
-  return KVQ_OK;
-}
 
 kvq_status kvq_quantize_kv_paged(const kvq_format* f, const kvq_paged_cache* pc, const void* k_src,
                                  const void* v_src, int64_t sb, int64_t sh, int64_t st, const int32_t* blocks,

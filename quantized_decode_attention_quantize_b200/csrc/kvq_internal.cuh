@@ -135,6 +135,85 @@ cudaError_t launch_decode_paged(const Layout& L, const PagedDecode& pd, int S, c
                                 float scale, float* ws_m, float* ws_l, float* ws_o, void* out, int out_dtype,
                                 int32_t* d_status, cudaStream_t s);
 
+// The pool's layout of a paged cache and the checks of its fixed fields (api.cu).
+kvq_status paged_layout(const kvq_format* f, const kvq_paged_cache* pc, Layout* L);
+
+// A rotation by a table; table = null for none.
+struct RopeArgs {
+  const float* table;
+  int64_t n_pos;
+  int rot, inter;
+};
+
+// Serving steps around the paged cache (rope.cu, paged.cu, attn_paged.cu).
+struct HeadRows {
+  const void* x;
+  void* y;
+  int64_t xt, xh, yt, yh;
+  int heads;
+  const void* weight;
+};
+cudaError_t launch_rope_table(const double* freq, int half, double amplitude, int64_t pos0, int64_t n_pos, float* table,
+                              cudaStream_t s);
+cudaError_t launch_norm_rope(int D, int dtype, int64_t n_tokens, const HeadRows& q, const HeadRows& k, float eps,
+                             float weight_offset, const RopeArgs& rope, const int32_t* positions, int32_t* d_status,
+                             cudaStream_t s);
+
+// The device-side numbers of a ragged batch over a paged cache.
+struct PagedBatch {
+  const int32_t* cu;        // [num_seqs + 1]
+  const int32_t* t_quant;   // [num_seqs]
+  const int32_t* t_res;     // [num_seqs]
+  const int32_t* table;     // [num_seqs][max_blocks]
+  int num_seqs, max_blocks, num_blocks, n_sink, res_cap;
+  int64_t n_rows, max_rows;
+};
+struct AppendArgs {
+  Layout L;                 // pool: one group per slab
+  PagedBatch b;
+  const void* src[2];
+  int64_t st[2], sh[2];
+  RopeArgs rope;
+  const int32_t* positions;
+  int32_t* t_quant_out;
+  int32_t* t_res_out;
+  void* sink[2];
+  void* res[2];
+  int32_t* status;
+};
+cudaError_t launch_append_paged(const AppendArgs& a, cudaStream_t s);
+struct ReadArgs {
+  Layout L;
+  PagedBatch b;
+  const int32_t* first;
+  void* out[2];
+  int out_dtype;
+  const void* sink[2];
+  const void* res[2];
+  int32_t* status;
+};
+cudaError_t launch_read_paged(const ReadArgs& a, cudaStream_t s);
+struct AttnArgs {
+  Layout L;
+  PagedBatch b;
+  int64_t max_t_quant;
+  int max_t_res;
+  const void* q;
+  int q_dtype, Hq, G;
+  float qscale;             // softmax scale * log2 e
+  int causal;
+  void* out;
+  int out_dtype;
+  float* lse;
+  void* ws;
+  const void* sink[2];
+  const void* res[2];
+  int32_t* status;
+};
+size_t attn_paged_workspace(int num_seqs, int Hq, int Hkv, int64_t n_rows, int64_t max_new, int64_t max_t_quant,
+                            int max_t_res, int n_sink);
+cudaError_t launch_attn_paged(const AttnArgs& a, cudaStream_t s);
+
 // ---------------------------------------------------------------------------
 // Device helpers
 // ---------------------------------------------------------------------------

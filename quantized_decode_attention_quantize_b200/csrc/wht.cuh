@@ -93,4 +93,29 @@ __device__ __forceinline__ void wht128_quad_unscaled(float (&x)[4], int lane) {
   }
 }
 
+// D = 128 with lane l of each half warp holding the octet 8 (l % 16) .. + 7: strides 1, 2, 4
+// within the lane, 8 .. 64 across lanes (partner lane ^ (h / 8)).  Without the final product.
+__device__ __forceinline__ void wht128_octet_unscaled(float (&x)[8], int lane) {
+#pragma unroll
+  for (int h = 1; h < 8; h <<= 1) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (!(j & h)) {
+        const float a = x[j], b = x[j + h];
+        x[j] = __fadd_rn(a, b);
+        x[j + h] = __fsub_rn(a, b);
+      }
+    }
+  }
+#pragma unroll
+  for (int hl = 1; hl < 16; hl <<= 1) {
+    const bool upper = lane & hl;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float o = __shfl_xor_sync(0xffffffffu, x[j], hl);
+      x[j] = upper ? __fsub_rn(o, x[j]) : __fadd_rn(x[j], o);
+    }
+  }
+}
+
 }  // namespace kvq

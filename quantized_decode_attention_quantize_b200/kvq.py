@@ -56,6 +56,25 @@ class kvq_paged_cache(ctypes.Structure):
                 ("res_k", ctypes.c_void_p), ("res_v", ctypes.c_void_p)]
 
 
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BANDS, ROPE_RAMP = range(4)
+
+
+class kvq_rope_spec(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("scaling", ctypes.c_int32)] + [
+        (n, ctypes.c_double) for n in ("base", "factor", "original_len", "low", "high", "amplitude")]
+
+
+class kvq_rope(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("n_pos", ctypes.c_int64), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
+
+
+class kvq_head_rows(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p)] + [
+        (n, ctypes.c_int64) for n in ("x_stride_t", "x_stride_h", "y_stride_t", "y_stride_h")] + [
+        ("heads", ctypes.c_int32), ("weight", ctypes.c_void_p)]
+
+
 class KvqError(RuntimeError):
     def __init__(self, fn, status):
         super().__init__(f"{fn}: {status_string(status)} ({status})")
@@ -104,6 +123,15 @@ def lib():
             "kvq_decode_paged_workspace_bytes": (SZ, [FP, I32, I32, I32, I64, I32]),
             "kvq_decode_attention_paged": (I32, [FP, PP, P, P, I64, I32, P, I32, I32, ctypes.c_float, P,
                                                  I32, P, SZ, P, P]),
+            "kvq_rope_table": (I32, [ctypes.POINTER(kvq_rope_spec), I64, I64, P, P]),
+            "kvq_norm_rope": (I32, [I32, I32, I64, ctypes.POINTER(kvq_head_rows), ctypes.POINTER(kvq_head_rows),
+                                    ctypes.c_float, ctypes.c_float, ctypes.POINTER(kvq_rope), P, P, P]),
+            "kvq_append_paged": (I32, [FP, PP, P, I64, I64, P, P, P, I64, I64, P, I64, I64,
+                                       ctypes.POINTER(kvq_rope), P, P, P, P, P]),
+            "kvq_read_paged": (I32, [FP, PP, P, I64, I64, P, P, P, P, P, I32, P, P]),
+            "kvq_attention_paged_workspace_bytes": (SZ, [FP, I32, I32, I32, I64, I64, I64, I32]),
+            "kvq_attention_paged": (I32, [FP, PP, P, I64, I64, P, P, I64, I32, P, I32, I32, ctypes.c_float, I32, P,
+                                          I32, P, P, SZ, P, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -159,10 +187,15 @@ class Cache:
     matrix [D][D] (stored as fp32)."""
 
     def __init__(self, fmt: kvq_format, B: int, H: int, C: int, device="cuda", k_lut=None,
-                 v_lut=None, sketch=None):
+                 v_lut=None, sketch=None, arrays=None):
         self.fmt, self.B, self.H, self.C = fmt, B, H, C
         self.tensors = {}
         self.struct = kvq_cache(batch=B, kv_heads=H, capacity=C)
+        if arrays is not None:   # the caller's tensors
+            self.tensors.update(arrays)
+            for name, t in arrays.items():
+                setattr(self.struct, name, t.data_ptr())
+            return
         for i, name in enumerate(ARRAYS):
             n = cache_array_bytes(fmt, B, H, C, i)
             if n:
@@ -347,17 +380,46 @@ class PagedCache:
     sink / residual arrays and a device block table [num_seqs][max_blocks] (int32, -1)."""
 
     def __init__(self, fmt: kvq_format, kv_heads: int, num_blocks: int, num_seqs: int, max_blocks: int,
-                 device="cuda"):
+                 device="cuda", arrays=None):
+        """arrays: name -> contiguous device tensor of the array's bytes (block_table: int32
+        [num_seqs][max_blocks]), used in place of new zeroed ones; they stay the caller's."""
         self.fmt, self.H, self.num_blocks = fmt, kv_heads, num_blocks
         self.num_seqs, self.max_blocks = num_seqs, max_blocks
-        self.pool = Cache(fmt, num_blocks, kv_heads, fmt.group_tokens, device=device)
-        raw = Cache(fmt, num_seqs, kv_heads, fmt.group_tokens, device=device)
-        self.raw = {n: raw.tensors[n] for n in ("sink_k", "sink_v", "res_k", "res_v") if n in raw.tensors}
-        self.block_table = torch.full((num_seqs, max_blocks), -1, dtype=torch.int32, device=device)
+        if arrays is None:
+            self.pool = Cache(fmt, num_blocks, kv_heads, fmt.group_tokens, device=device)
+            raw = Cache(fmt, num_seqs, kv_heads, fmt.group_tokens, device=device)
+            self.raw = {n: raw.tensors[n] for n in ("sink_k", "sink_v", "res_k", "res_v") if n in raw.tensors}
+            self.block_table = torch.full((num_seqs, max_blocks), -1, dtype=torch.int32, device=device)
+        else:
+            self.pool = Cache(fmt, num_blocks, kv_heads, fmt.group_tokens, arrays=self._part(arrays, False, num_blocks))
+            self.raw = self._part(arrays, True, num_seqs)
+            self.block_table = arrays["block_table"]
+            if self.block_table.dtype != torch.int32 or tuple(self.block_table.shape) != (num_seqs, max_blocks) or \
+                    not self.block_table.is_contiguous():
+                raise ValueError("block_table must be a contiguous int32 [num_seqs][max_blocks]")
         self.struct = kvq_paged_cache(pool=self.pool.struct, num_seqs=num_seqs, max_blocks=max_blocks,
                                       block_table=self.block_table.data_ptr())
         for n, t in self.raw.items():
             setattr(self.struct, n, t.data_ptr())
+
+    def _part(self, arrays, per_seq, slabs):
+        """The given pool (or per-sequence raw) arrays, each of the size the format asks for."""
+        got = {}
+        for i, n in enumerate(ARRAYS):
+            if (n in ("sink_k", "sink_v", "res_k", "res_v")) != per_seq:
+                continue
+            need = cache_array_bytes(self.fmt, slabs, self.H, self.fmt.group_tokens, i)
+            if not need:
+                continue
+            t = arrays.get(n)
+            if t is None or not t.is_contiguous() or t.numel() * t.element_size() != need:
+                raise ValueError(f"{n}: a contiguous tensor of {need} bytes is needed")
+            got[n] = t
+        return got
+
+    @property
+    def device(self):
+        return self.block_table.device
 
     def array(self, name):
         return self.raw[name] if name in self.raw else self.pool.tensors[name]
@@ -395,4 +457,209 @@ def decode_attention_paged(fmt, cache: PagedCache, t_quant: torch.Tensor, t_res:
                                           max_t_res, _ptr(q), KVQ_DTYPE[q.dtype], Hq, scale, _ptr(out), out_dtype,
                                           _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream))
     _check("kvq_decode_attention_paged", st)
+    return out
+
+
+# ---- serving steps around the paged cache ---------------------------------------------------
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+class _On:
+    """The device of a call made current for its launch (and its stream for new tensors)."""
+
+    def __init__(self, device, stream):
+        _need(device.type == "cuda", "the tensors must be on a CUDA device")
+        _need(stream is None or stream.device == device, "the stream is on another device than the tensors")
+        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        self.stream = None if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        if self.stream is not None:
+            self.stream.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *e):
+        if self.stream is not None:
+            self.stream.__exit__(*e)
+        if self.guard is not None:
+            self.guard.__exit__(*e)
+
+
+def _ints(t, n, device, what):
+    _need(t.dtype == torch.int32 and t.dim() == 1 and t.numel() == n and t.is_contiguous() and t.device == device,
+          f"{what}: a contiguous int32 tensor of {n} values on the same device is needed")
+    return t.data_ptr()
+
+
+def _status_ptr(status, device):
+    if status is None:
+        return None
+    return _ints(status, 1, device, "status")
+
+
+def make_rope_spec(rot_dim: int, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, original_len=0.0, low=0.0, high=0.0,
+                   amplitude=1.0) -> kvq_rope_spec:
+    return kvq_rope_spec(rot_dim=rot_dim, scaling=scaling, base=base, factor=factor, original_len=original_len,
+                         low=low, high=high, amplitude=amplitude)
+
+
+def rope_table(spec: kvq_rope_spec, n_pos: int, pos0=0, out=None, device="cuda", stream=None):
+    """kvq_rope_table: fp32 [n_pos, rot_dim], cosines then sines of each position."""
+    if out is not None:
+        device = out.device
+        _need(out.dtype == torch.float32 and tuple(out.shape) == (n_pos, spec.rot_dim) and out.is_contiguous(),
+              "out: a contiguous fp32 [n_pos, rot_dim] tensor is needed")
+    else:
+        _need(n_pos >= 0, "n_pos must not be negative")
+        device = torch.device(device)
+        if device.type == "cuda" and device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+    with _On(device, stream) as s:
+        if out is None:
+            out = torch.empty((n_pos, spec.rot_dim), dtype=torch.float32, device=device)
+        _check("kvq_rope_table", lib().kvq_rope_table(spec, pos0, n_pos, out.data_ptr(), s))
+    return out
+
+
+class Rope:
+    """A rotation by the rows of `table` (fp32 [n_pos, rot_dim], see rope_table)."""
+
+    def __init__(self, table: torch.Tensor, interleaved=False):
+        _need(table.dtype == torch.float32 and table.dim() == 2 and table.is_contiguous(),
+              "table: a contiguous fp32 [n_pos, rot_dim] tensor is needed")
+        self.table = table
+        self.struct = kvq_rope(table=table.data_ptr(), n_pos=table.shape[0], rot_dim=table.shape[1],
+                               interleaved=int(interleaved))
+
+
+def _rope_ptr(rope, device):
+    if rope is None:
+        return None
+    _need(rope.table.device == device, "the rotary table is on another device")
+    return rope.struct
+
+
+def _head_rows(x, y, weight, what):
+    _need(x.dim() == 3 and x.stride(2) == 1, f"{what}: [tokens, heads, head_dim] with contiguous channels is needed")
+    _need(y.shape == x.shape and y.dtype == x.dtype and y.device == x.device and y.stride(2) == 1,
+          f"{what}: the output's shape, dtype or device differs")
+    if weight is not None:
+        _need(weight.dtype == x.dtype and weight.dim() == 1 and weight.numel() == x.shape[2] and
+              weight.is_contiguous() and weight.device == x.device,
+              f"{what}: a weight of [head_dim] in the rows' dtype is needed")
+    xt, xh, _ = x.stride()
+    yt, yh, _ = y.stride()
+    return kvq_head_rows(x.data_ptr(), y.data_ptr(), xt, xh, yt, yh, x.shape[1],
+                         None if weight is None else weight.data_ptr())
+
+
+def norm_rope(q: torch.Tensor, k=None, q_weight=None, k_weight=None, eps=1e-6, weight_offset=0.0, rope=None,
+              positions=None, q_out=None, k_out=None, status=None, stream=None):
+    """kvq_norm_rope: q [T, Hq, D] and k [T, Hk, D] (strided over tokens and heads) -> both
+    normed per head (with a weight) and turned at `positions` (int32 [T]).  q_out = q and
+    k_out = k work in place; new contiguous tensors otherwise."""
+    _need(q.dtype in KVQ_DTYPE and q.dim() == 3, "q: [tokens, heads, head_dim] in fp32, fp16 or bf16 is needed")
+    T, _, D = q.shape
+    if k is not None:
+        _need(k.dim() == 3 and k.shape[0] == T and k.shape[2] == D and k.dtype == q.dtype and k.device == q.device,
+              "k: the tokens, head_dim, dtype and device of q are needed")
+    else:
+        _need(k_weight is None and k_out is None, "k_weight and k_out go with k")
+    with _On(q.device, stream) as s:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        rows_q = _head_rows(q, q_out, q_weight, "q")
+        rows_k = None if k is None else _head_rows(k, k_out, k_weight, "k")
+        pos = None if positions is None else _ints(positions, T, q.device, "positions")
+        _check("kvq_norm_rope", lib().kvq_norm_rope(D, KVQ_DTYPE[q.dtype], T, rows_q, rows_k, eps, weight_offset,
+                                                    _rope_ptr(rope, q.device), pos, _status_ptr(status, q.device), s))
+    return q_out, k_out
+
+
+def _batch(cache, cu, t_quant, t_res):
+    d, n = cache.device, cache.num_seqs
+    return (_ints(cu, n + 1, d, "cu"), _ints(t_quant, n, d, "t_quant"), _ints(t_res, n, d, "t_res"))
+
+
+def append_paged(fmt, cache: PagedCache, cu_new: torch.Tensor, max_new: int, t_quant: torch.Tensor,
+                 t_res: torch.Tensor, k_src: torch.Tensor, v_src: torch.Tensor, t_quant_out: torch.Tensor,
+                 t_res_out: torch.Tensor, rope=None, positions=None, status=None, stream=None):
+    """kvq_append_paged: k_src, v_src [rows, Hkv, D] (strided over rows and heads), the rows
+    [cu_new[s], cu_new[s + 1]) following what sequence s holds; the lengths after it go to
+    t_quant_out / t_res_out."""
+    dt, d = TORCH_DTYPE[fmt.src_dtype], cache.device
+    rows = k_src.shape[0]
+    for x, what in ((k_src, "k_src"), (v_src, "v_src")):
+        _need(tuple(x.shape) == (rows, cache.H, fmt.head_dim) and x.dtype == dt and x.device == d and x.stride(2) == 1,
+              f"{what}: [rows, kv_heads, head_dim] in the format's source dtype is needed")
+    cu, tq, tr = _batch(cache, cu_new, t_quant, t_res)
+    tq_o, tr_o = _ints(t_quant_out, cache.num_seqs, d, "t_quant_out"), _ints(t_res_out, cache.num_seqs, d, "t_res_out")
+    pos = None if positions is None else _ints(positions, rows, d, "positions")
+    with _On(d, stream) as s:
+        _check("kvq_append_paged", lib().kvq_append_paged(
+            fmt, cache.struct, cu, rows, max_new, tq, tr, k_src.data_ptr(), k_src.stride(0), k_src.stride(1),
+            v_src.data_ptr(), v_src.stride(0), v_src.stride(1), _rope_ptr(rope, d), pos, tq_o, tr_o,
+            _status_ptr(status, d), s))
+
+
+def read_paged(fmt, cache: PagedCache, cu: torch.Tensor, max_rows: int, first: torch.Tensor, t_quant: torch.Tensor,
+               t_res: torch.Tensor, n_rows: int, out_dtype=None, k_out=None, v_out=None, status=None, stream=None):
+    """kvq_read_paged: the tokens at positions first[s], ... of every sequence as rows
+    [cu[s], cu[s + 1]) -> k, v [n_rows, Hkv, D] (out_dtype: the source dtype by default)."""
+    d = cache.device
+    out_dtype = fmt.src_dtype if out_dtype is None else out_dtype
+    shape, dt = (n_rows, cache.H, fmt.head_dim), TORCH_DTYPE[out_dtype]
+    cu, tq, tr = _batch(cache, cu, t_quant, t_res)
+    p0 = _ints(first, cache.num_seqs, d, "first")
+    for x in (k_out, v_out):
+        _need(x is None or (tuple(x.shape) == shape and x.dtype == dt and x.device == d and x.is_contiguous()),
+              "k_out / v_out: contiguous [n_rows, kv_heads, head_dim] in out_dtype is needed")
+    with _On(d, stream) as s:
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=dt, device=d)
+        if v_out is None:
+            v_out = torch.empty(shape, dtype=dt, device=d)
+        _check("kvq_read_paged", lib().kvq_read_paged(fmt, cache.struct, cu, n_rows, max_rows, p0, tq, tr,
+                                                      k_out.data_ptr(), v_out.data_ptr(), out_dtype,
+                                                      _status_ptr(status, d), s))
+    return k_out, v_out
+
+
+def attention_paged_workspace_bytes(fmt, num_seqs, Hq, Hkv, n_rows, max_new, max_t_quant, max_t_res) -> int:
+    return lib().kvq_attention_paged_workspace_bytes(fmt, num_seqs, Hq, Hkv, n_rows, max_new, max_t_quant, max_t_res)
+
+
+def attention_paged(fmt, cache: PagedCache, cu_q: torch.Tensor, max_new: int, t_quant: torch.Tensor,
+                    t_res: torch.Tensor, max_t_quant: int, max_t_res: int, q: torch.Tensor, scale: float, causal=True,
+                    out_dtype=None, out=None, lse=None, workspace=None, status=None, stream=None):
+    """kvq_attention_paged: q [rows, Hq, D] contiguous, the last cu_q[s + 1] - cu_q[s] tokens of
+    every sequence -> out [rows, Hq, D] (out_dtype: q's by default); lse: fp32 [rows, Hq]."""
+    d = cache.device
+    _need(q.dtype in KVQ_DTYPE and q.dim() == 3 and q.shape[2] == fmt.head_dim and q.is_contiguous() and q.device == d,
+          "q: a contiguous [rows, q_heads, head_dim] in fp32, fp16 or bf16 is needed")
+    rows, Hq, _ = q.shape
+    out_dtype = KVQ_DTYPE[q.dtype] if out_dtype is None else out_dtype
+    _need(out is None or (out.shape == q.shape and out.dtype == TORCH_DTYPE[out_dtype] and out.device == d and
+                          out.is_contiguous()), "out: a contiguous tensor of q's shape in out_dtype is needed")
+    _need(lse is None or (tuple(lse.shape) == (rows, Hq) and lse.dtype == torch.float32 and lse.device == d and
+                          lse.is_contiguous()), "lse: a contiguous fp32 [rows, q_heads] tensor is needed")
+    cu, tq, tr = _batch(cache, cu_q, t_quant, t_res)
+    with _On(d, stream) as s:
+        if out is None:
+            out = torch.empty(q.shape, dtype=TORCH_DTYPE[out_dtype], device=d)
+        if workspace is None:
+            need = attention_paged_workspace_bytes(fmt, cache.num_seqs, Hq, cache.H, rows, max_new, max_t_quant,
+                                                   max_t_res)
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=d)
+        _need(workspace.is_contiguous() and workspace.device == d, "workspace: a contiguous tensor on q's device")
+        _check("kvq_attention_paged", lib().kvq_attention_paged(
+            fmt, cache.struct, cu, rows, max_new, tq, tr, max_t_quant, max_t_res, q.data_ptr(), KVQ_DTYPE[q.dtype],
+            Hq, scale, int(causal), out.data_ptr(), out_dtype, None if lse is None else lse.data_ptr(),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), _status_ptr(status, d), s))
     return out
