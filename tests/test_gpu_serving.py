@@ -36,6 +36,7 @@ from tests.gpu_util import TORCH, dev
 pytestmark = pytest.mark.gpu
 U = {F32: 2.0 ** -24, F16: 2.0 ** -11, BF16: 2.0 ** -8}
 POOL = ("k_codes", "k_scale", "k_zero", "v_codes", "v_scale", "v_zero")
+WHT = np.array([[(-1.0) ** bin(i & j).count("1") for j in range(128)] for i in range(128)]) / np.sqrt(128)
 RAW = ("sink_k", "sink_v", "res_k", "res_v")
 
 
@@ -250,7 +251,10 @@ class Paged:
                     continue
                 for hq in range(out.shape[1]):
                     k, v = K[hq // G, :seen], V[hq // G, :seen]
-                    d = (2 * u + u * u) * scale * np.max(np.abs(k) @ np.abs(qs[i, hq]))
+                    # the operands as they are rounded: in the transformed basis for rotating formats
+                    # (the same products, but other magnitudes: the error bound is not invariant)
+                    qb, kb = (qs[i, hq], k) if not self.fd["k_rotate"] else (qs[i, hq] @ WHT, k @ WHT)
+                    d = (2 * u + u * u) * scale * np.max(np.abs(kb) @ np.abs(qb))
                     p = np.exp(scale * k @ qs[i, hq] - rl[i, hq])
                     bar = ((1 + 2 * u) * (1 + 2.0 ** -16) * np.exp(2 * d) - 1) * (p @ np.abs(v))
                     bar = bar + (U[out_dt] if out_dt != F32 else 0) * (np.abs(ref[i, hq]) + bar) + 1e-7
@@ -258,7 +262,7 @@ class Paged:
                     assert np.all(err <= bar), (s, i, hq, float(np.max(err / bar)))
                     if lse is not None:
                         assert abs(lse[cu[s] + i, hq] - rl[i, hq]) <= d + 2.0 ** -16 * (1 + abs(rl[i, hq]))
-                    worst = max(worst, scale ** 2 * float(p @ (k * k) @ (qs[i, hq] ** 2)))
+                    worst = max(worst, scale ** 2 * float(p @ (kb * kb) @ (qb ** 2)))
                     num, den = num + float(err @ err), den + float(ref[i, hq] @ ref[i, hq])
             if den:
                 bar = 4 * np.sqrt(u * u / 3 * (2 * worst + 2)) + (U[out_dt] if out_dt != F32 else 0)
