@@ -224,7 +224,7 @@ static kvq_status attn_sizes(const kvq_format* f, int32_t num_seqs, int32_t Hq, 
 size_t kvq_attention_paged_workspace_bytes(const kvq_format* f, int32_t num_seqs, int32_t Hq, int32_t Hkv,
                                            int64_t n_rows, int64_t max_new, int64_t max_tq, int32_t max_tr) {
   if (attn_sizes(f, num_seqs, Hq, Hkv, n_rows, max_new, max_tq, max_tr) != KVQ_OK) return 0;
-  return attn_paged_workspace(num_seqs, Hq, Hkv, n_rows, max_new, max_tq, max_tr, f->n_sink);
+  return attn_paged_workspace(Hq / Hkv, max_new);
 }
 
 kvq_status kvq_attention_paged(const kvq_format* f, const kvq_paged_cache* pc, const int32_t* cu, int64_t n_rows,
@@ -244,8 +244,7 @@ kvq_status kvq_attention_paged(const kvq_format* f, const kvq_paged_cache* pc, c
   if (!aligned(lse, 4)) return KVQ_ERR_INVALID;
   if (n_rows && (!q || !out || !aligned(q, 16) || !aligned(out, 16))) return KVQ_ERR_INVALID;
   if (!ws || !aligned(ws, 16)) return KVQ_ERR_INVALID;
-  if (ws_bytes < attn_paged_workspace(pc->num_seqs, Hq, a.L.Hkv, n_rows, max_new, max_tq, max_tr, a.L.n_sink))
-    return KVQ_ERR_WORKSPACE;
+  if (ws_bytes < attn_paged_workspace(Hq / a.L.Hkv, max_new)) return KVQ_ERR_WORKSPACE;
   if (n_rows == 0 || max_new == 0) return KVQ_OK;
   a.max_t_quant = max_tq;
   a.max_t_res = max_tr;

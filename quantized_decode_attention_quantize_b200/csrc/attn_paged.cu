@@ -2,12 +2,16 @@
 // tokens, 4-bit per-channel keys, 2-bit per-token values, raw sink and window rows) on the
 // fifth-generation tensor cores.
 //
-// Work.  The query rows of one KV head, G per new token, are cut into blocks of up to 256.  A
-// CTA takes one block over a run of KV tiles of 128 tokens: the visible raw (sink, window)
-// tokens first, then the visible packed groups.  It keeps two streams busy, so that one's
-// products run under the other's softmax: the block's two halves of 128 rows over the same
-// tiles, or, for a block of at most 128 rows, those rows over the even and the odd tiles, the
-// two states merged at the end.
+// Work.  The query rows of one KV head, G per new token, are cut into blocks of up to 256; a
+// block sees KV tiles of 128 tokens: its visible raw (sink, window) tokens first, then its
+// visible packed groups.  The tiles of all blocks end to end, each block with one more unit for its
+// fixed costs, are cut into equal runs, one per SM, whatever the lengths in the batch.  A block that
+// one run holds whole is written out at once; of a block cut by runs every part leaves its softmax
+// state in the workspace, and a second kernel, one CTA per cut, merges them.
+//
+// Within a block two streams keep the tensor core busy, so that one's products run under the
+// other's softmax: the block's two halves of 128 rows over the same tiles, or, for a block of at
+// most 128 rows, those rows over the even and the odd tiles, the two states merged at the end.
 //
 // Mathematics.  S = Q K^T and O += P V as products of fp16 with fp32 sums, one pass over the
 // tiles with a running maximum m and sum l per row in the log2 domain.  m moves (and O, l are
@@ -18,12 +22,19 @@
 // number 2^(10 - p) (p the bit it starts at) is 2^(10 - p) + c exactly; less that constant, one fused
 // c * s + z gives the fp16 key or value.
 //
-// Roles (16 warps).  Warps 0-3 and 4-7: softmax of stream 0 and 1, one thread per row, S in registers
-// from tensor memory, P back over S's columns as the A operand of the value product.  Warps
-// 8-11: codes from global memory (one tile ahead, in registers) to fp16 tiles in shared
-// memory, K as [token][channel] with the channels of an octet in the order 0 4 1 5 2 6 3 7 (which
-// the masks give; Q has the same), V transposed to [channel][token].  Warp 12: one thread issues the
-// products.  K and V tiles pass through one ring of four slots in the order the products use them.
+// Roles (26 warps).
+//   0-15   softmax: stream w = warp / 8, two threads per row (64 columns each, the maxima exchanged in
+//          shared memory); S from tensor memory in chunks of 32 columns, P back over S's columns
+//          32-95 as the A operand of the value product.  They also stage the queries and write the
+//          output.
+//   16-19  keys: codes to an fp16 tile [token][channel], the channels of an octet in the order 0 4
+//          1 5 2 6 3 7 (which the masks give; Q has the same).
+//   20-23  values: codes to an fp16 tile [channel][token], channel 8 W + c in row 16 c + W (rows of
+//          a store phase then differ modulo 8, and their chunks in bank).
+//   24     one thread issues the products.
+//   25     finds the run's blocks, announces them, and copies the packed groups' codes and metadata
+//          into shared memory (bulk copies, two groups ahead).
+// K and V tiles pass through one ring of four slots in the order the products use them.
 //
 // Tensor memory: S0, S1, O0, O1, 128 columns each (all 512).  A product that overwrites S with the
 // next scores is issued after the value product that reads P from it, in the same thread's order.
@@ -37,22 +48,48 @@ namespace kvq {
 namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kThreads = 512;
+constexpr int kThreads = 832;
 constexpr int kTile = 32768;              // 128 x 128 fp16
 constexpr int kSlots = 4;
 constexpr int kSlotsAt = 2 * kTile;       // after the two Q tiles
-constexpr int kSmallAt = kSlotsAt + kSlots * kTile;
+constexpr int kStages = 2;                // packed groups in flight
+constexpr int kStageK = 8192 + 512, kStageV = 4096 + 512;   // codes, scales, zero-points
+constexpr int kStagesAt = kSlotsAt + kSlots * kTile;
+constexpr int kSmallAt = kStagesAt + kStages * (kStageK + kStageV);
+constexpr int kSegs = 2;                  // announced blocks
 constexpr float kLazy = 8.0f;             // log2 slack of the running maximum
 constexpr float kLift = 7.0f;             // log2 factor carried by the weights
+constexpr int kMinRun = 4;                // units of a run at least
+
+// The part of a block that this CTA does.
+struct Seg {
+  int64_t row0;        // the sequence's first query row
+  int s, h, n, tq, tr;
+  int r0, nr;          // rows of the block within the sequence's n * G
+  int split;           // one half block, tiles dealt to the streams in turn
+  int n_raw;           // raw tiles of the block
+  int t_lo, N;         // tiles [t_lo, t_lo + N); N = 0: nothing to see; N < 0: no more blocks
+  int raw, packed;     // tokens the block's last row sees
+  int slot;            // partial slot, or -1 for the output itself
+};
 
 struct Small {
   float rowscale[256];
+  float mx[2][2][128];                    // [stream][half][row]: maxima, at the end sums
   float m1[128], l1[128];                 // stream 1's state on its way to stream 0
-  alignas(8) uint64_t full[kSlots], empty[kSlots], s_full[2], p_full[2], o_full[2], drain;
+  Seg seg[kSegs];
+  alignas(8) uint64_t full[kSlots], empty[kSlots];
+  uint64_t k_in[kStages], k_out[kStages], v_in[kStages], v_out[kStages];
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
+  uint64_t s_full[2], p_full[2], o_full[2], q_full, drain;
+  uint64_t row_pair[8];                   // the two warps of a stream's 32 rows
+  uint64_t row_quad[4];                   // the four warps of both streams with the same rows
+  uint64_t all;                           // the 16 softmax warps
   uint32_t tmem;
   int stop;
 };
 constexpr size_t kSmem = kSmallAt + sizeof(Small);
+static_assert(kSmem <= 232448, "shared memory of a CTA");
 
 struct AttnSeq {
   int64_t row0;
@@ -73,11 +110,6 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int s) {
   return q;
 }
 
-// Row blocks of a sequence (one for a sequence to be refused, so that a CTA sees it).
-__device__ __forceinline__ int attn_blocks(const AttnArgs& a, int s) {
-  const AttnSeq q = attn_seq(a, s);
-  return q.ok ? (int)(((int64_t)q.n * a.G + 255) / 256) : 1;
-}
 
 // What one query row sees: the first `raw` raw tokens (sink, then window) and the first `packed`
 // packed ones.
@@ -95,16 +127,148 @@ __device__ __forceinline__ Seen row_seen(const AttnArgs& a, const AttnSeq& q, in
   return r;
 }
 
-struct Cta {
-  int s, h;
-  int r0, nr;          // its rows of the sequence's n * G
-  bool split;          // one half block, tiles dealt to the streams in turn
-  int n_raw;           // raw tiles
-  int t_lo, N;         // its tiles [t_lo, t_lo + N) of the block's
-  int raw, packed;     // tokens its last row sees
+// Row blocks of a sequence and the KV tiles the last row of block b sees.
+__device__ __forceinline__ int seq_blocks(const AttnArgs& a, const AttnSeq& q) {
+  return (int)(((int64_t)q.n * a.G + 255) / 256);
+}
+__device__ __forceinline__ int block_tiles(const AttnArgs& a, const AttnSeq& q, int b) {
+  const int64_t last = min((int64_t)q.n * a.G, (int64_t)(b + 1) * 256) - 1;
+  const Seen v = row_seen(a, q, (int)(last / a.G));
+  return (v.raw + 127) / 128 + (v.packed + 127) / 128;
+}
+
+// ---- the partition (one warp) ----------------------------------------------------------------
+// Units of a sequence's blocks (per KV head): tiles + 1 each.  `q` differs from lane to lane.
+__device__ __forceinline__ int64_t seq_units(const AttnArgs& a, const AttnSeq& q, int lane) {
+  const int nb = q.ok ? seq_blocks(a, q) : 0;
+  int64_t w = nb == 1 ? block_tiles(a, q, 0) + 1 : 0;
+  unsigned many = __ballot_sync(0xffffffffu, nb > 1);
+  while (many) {   // sequences of several blocks: a lane per block
+    const int l = __ffs(many) - 1;
+    many &= many - 1;
+    AttnSeq o = q;
+    o.n = __shfl_sync(0xffffffffu, q.n, l);
+    o.tq = __shfl_sync(0xffffffffu, q.tq, l);
+    o.tr = __shfl_sync(0xffffffffu, q.tr, l);
+    const int ob = seq_blocks(a, o);
+    int64_t sum = 0;
+    for (int b = lane; b < ob; b += 32) sum += block_tiles(a, o, b) + 1;
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    if (lane == l) w = sum;
+  }
+  return w;
+}
+__device__ __forceinline__ int64_t scan64(int64_t v, int lane) {   // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+// All units, and the number of runs they are cut into.
+struct Cut {
+  int64_t units;
+  int runs;
+};
+__host__ __device__ __forceinline__ int64_t run_start(const Cut& c, int i) {
+  return (int64_t)((__int128)c.units * i / c.runs);
+}
+__device__ __forceinline__ Cut find_cut(const AttnArgs& a, int lane) {
+  int64_t total = 0;
+  bool bad = false;
+  for (int s0 = 0; s0 < a.b.num_seqs; s0 += 32) {
+    AttnSeq q = {};
+    if (s0 + lane < a.b.num_seqs) {
+      q = attn_seq(a, s0 + lane);
+      bad |= !q.ok;
+    }
+    total += __shfl_sync(0xffffffffu, scan64(seq_units(a, q, lane), lane), 31);
+  }
+  if (blockIdx.x == 0 && __any_sync(0xffffffffu, bad) && lane == 0) flag(a.status, KVQ_DEV_BOUNDS);
+  Cut c;
+  c.units = total * a.L.Hkv;
+  c.runs = (int)max((int64_t)1, min((int64_t)gridDim.x, c.units / kMinRun));
+  return c;
+}
+
+// A place in the list of blocks: sequence s, its block b (the last, which sees the most, comes first), head h.
+struct Place {
+  AttnSeq q;
+  int s, b, h;
+};
+__device__ __forceinline__ bool next_seq(const AttnArgs& a, Place* p) {   // the first from p->s on that has rows
+  for (; p->s < a.b.num_seqs; ++p->s) {
+    p->q = attn_seq(a, p->s);
+    if (p->q.ok && p->q.n > 0) {
+      p->b = seq_blocks(a, p->q) - 1;
+      p->h = 0;
+      return true;
+    }
+  }
+  return false;
+}
+__device__ __forceinline__ bool next_block(const AttnArgs& a, Place* p) {
+  if (++p->h < a.L.Hkv) return true;
+  p->h = 0;
+  if (--p->b >= 0) return true;
+  ++p->s;
+  return next_seq(a, p);
+}
+// The block that holds unit `at`, and the unit's index in it.
+__device__ __forceinline__ Place find_place(const AttnArgs& a, int64_t at, int lane, int64_t* unit) {
+  Place p = {};
+  for (int s0 = 0; s0 < a.b.num_seqs; s0 += 32) {
+    AttnSeq q = {};
+    if (s0 + lane < a.b.num_seqs) q = attn_seq(a, s0 + lane);
+    const int64_t w = seq_units(a, q, lane) * a.L.Hkv, incl = scan64(w, lane);
+    const unsigned hit = __ballot_sync(0xffffffffu, at < incl);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      at -= __shfl_sync(0xffffffffu, incl - w, l);
+      p.s = s0 + l;
+      break;
+    }
+    at -= __shfl_sync(0xffffffffu, incl, 31);
+  }
+  p.q = attn_seq(a, p.s);
+  const int nb = seq_blocks(a, p.q);
+  for (int b0 = nb - 1;; b0 -= 32) {   // lanes take blocks b0, b0 - 1, ...
+    const int64_t w = b0 - lane >= 0 ? (int64_t)(block_tiles(a, p.q, b0 - lane) + 1) * a.L.Hkv : 0;
+    const int64_t incl = scan64(w, lane);
+    const unsigned hit = __ballot_sync(0xffffffffu, at < incl);
+    if (hit || b0 < 32) {
+      const int l = hit ? __ffs(hit) - 1 : b0;
+      at -= __shfl_sync(0xffffffffu, incl - w, l);
+      p.b = b0 - l;
+      const int64_t one = __shfl_sync(0xffffffffu, w, l) / a.L.Hkv;
+      p.h = (int)(at / one);
+      *unit = at % one;
+      return p;
+    }
+    at -= __shfl_sync(0xffffffffu, incl, 31);
+  }
+}
+
+// The workspace: the cut, every run's first block, and two partial slots per run (2 i: the rest of a block
+// that an earlier run began; 2 i + 1: the beginning of one that run i does not finish).
+struct First {
+  int64_t row0;
+  int h, r0, nr, pad;
+  int64_t unit, units;   // where in its block the run starts, and the block's units
+};
+struct Work {
+  Cut* cut;
+  First* first;
+  int rows;              // of a slot
+  float* m;              // [slots][rows]
+  float* l;
+  float* o;              // [slots][rows][128]
 };
 
-// ---- producer: codes to fp16 tiles -------------------------------------------------------
+// ---- producers: codes to fp16 tiles ------------------------------------------------------------
 __device__ __forceinline__ uint32_t h2sub(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -120,115 +284,73 @@ __device__ __forceinline__ uint32_t hi2(uint32_t a, uint32_t b) { return __byte_
 __device__ __forceinline__ void st16(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
-__device__ __forceinline__ uint4 ldg16(const void* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
-__device__ __forceinline__ uint2 ldg8(const void* p) { return __ldg(reinterpret_cast<const uint2*>(p)); }
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// A packed group's keys as thread t of 128 takes them: words 4 (t % 4) .. + 3 (32 channels) of tokens
-// t / 4 + 32 j, and those channels' scales and zero-points.
-struct KCodes {
-  uint4 w[4], s[4], z[4];
-};
-__device__ __forceinline__ void load_k(const AttnArgs& a, int64_t slab, int t, KCodes& k) {
-  const uint8_t* c = reinterpret_cast<const uint8_t*>(a.L.side[0].codes) + slab * a.L.side[0].code_slab_bytes;
-  const __half* s = reinterpret_cast<const __half*>(a.L.side[0].scale) + slab * 128 + 32 * (t & 3);
-  const __half* z = reinterpret_cast<const __half*>(a.L.side[0].zero) + slab * 128 + 32 * (t & 3);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    k.w[j] = ldg16(c + ((t >> 2) + 32 * j) * 64 + (t & 3) * 16);
-    k.s[j] = ldg16(s + 8 * j);
-    k.z[j] = ldg16(z + 8 * j);
-  }
-}
-__device__ __forceinline__ void put_k(const KCodes& k, uint32_t slot, int t) {
-  const int q = t & 3;
-  const uint32_t base = slot + (q >> 1) * 16384;
-#pragma unroll
-  for (int ii = 0; ii < 4; ++ii) {
-    // the eight lanes of a store phase cover two tokens and four quads: quads of one half start
-    // two chunks apart, which keeps their 16-byte chunks in different banks
-    const uint4 sr = (ii == 0) ? (q < 2 ? k.s[0] : k.s[2]) : (ii == 1) ? (q < 2 ? k.s[1] : k.s[3])
-                   : (ii == 2) ? (q < 2 ? k.s[2] : k.s[0]) : (q < 2 ? k.s[3] : k.s[1]);
-    const uint4 zr = (ii == 0) ? (q < 2 ? k.z[0] : k.z[2]) : (ii == 1) ? (q < 2 ? k.z[1] : k.z[3])
-                   : (ii == 2) ? (q < 2 ? k.z[2] : k.z[0]) : (q < 2 ? k.z[3] : k.z[1]);
-    const int i = q < 2 ? ii : (ii + 2) & 3;
-    const uint32_t s0 = lo2(sr.x, sr.z), s1 = hi2(sr.x, sr.z), s2 = lo2(sr.y, sr.w), s3 = hi2(sr.y, sr.w);
-    const uint32_t z0 = lo2(zr.x, zr.z), z1 = hi2(zr.x, zr.z), z2 = lo2(zr.y, zr.w), z3 = hi2(zr.y, zr.w);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint4 wj = k.w[j];
-      const uint32_t w = (ii == 0) ? (q < 2 ? wj.x : wj.z) : (ii == 1) ? (q < 2 ? wj.y : wj.w)
-                       : (ii == 2) ? (q < 2 ? wj.z : wj.x) : (q < 2 ? wj.w : wj.y);
-      const uint32_t v = w >> 8;
-      const int r = (t >> 2) + 32 * j, c = 4 * (q & 1) + i;
-      st16(base + r * 128 + ((c ^ (r & 7)) << 4),
-           h2fma(h2sub((w & 0x000F000Fu) | 0x64006400u, 0x64006400u), s0, z0),
-           h2fma(h2sub((w & 0x00F000F0u) | 0x54005400u, 0x54005400u), s1, z1),
-           h2fma(h2sub((v & 0x000F000Fu) | 0x64006400u, 0x64006400u), s2, z2),
-           h2fma(h2sub((v & 0x00F000F0u) | 0x54005400u, 0x54005400u), s3, z3));
-    }
-  }
-}
-
-// A packed group's values as thread t takes them: words 2 (t / 16), + 1 (16 channels) of the token octet
-// t % 16 (pairs 4 (t % 16) + j), and those tokens' scales and zero-points.
-struct VCodes {
-  uint2 w[4];
-  uint4 s, z;
-};
-__device__ __forceinline__ void load_v(const AttnArgs& a, int64_t slab, int t, VCodes& v) {
-  const uint8_t* c = reinterpret_cast<const uint8_t*>(a.L.side[1].codes) + slab * a.L.side[1].code_slab_bytes;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) v.w[j] = ldg8(c + (4 * (t & 15) + j) * 64 + (t >> 4) * 8);
-  v.s = ldg16(reinterpret_cast<const __half*>(a.L.side[1].scale) + slab * 128 + 8 * (t & 15));
-  v.z = ldg16(reinterpret_cast<const __half*>(a.L.side[1].zero) + slab * 128 + 8 * (t & 15));
-}
+// Two codes of w under MASK, whose bit positions MAGIC's exponents make units, times s plus z.
 template <uint32_t MASK, uint32_t MAGIC>
 __device__ __forceinline__ uint32_t code2(uint32_t w, uint32_t s, uint32_t z) {
   return h2fma(h2sub((w & MASK) | MAGIC, MAGIC), s, z);
 }
-__device__ __forceinline__ void put_v(const VCodes& v, uint32_t slot, int t, int valid) {
-  const int o = t & 15;
-  const uint32_t base = slot + (o >> 3) * 16384;
-  uint32_t s[4] = {v.s.x, v.s.y, v.s.z, v.s.w}, z[4] = {v.z.x, v.z.y, v.z.z, v.z.w};
+
+// A packed group's keys: thread t of 128 takes octet t % 16 (one word) of tokens t / 16 + 8 j.  The eight
+// lanes of a store phase hold eight octets of one token, whose chunks lie in different banks.
+__device__ __forceinline__ void put_keys(const uint8_t* stage, uint32_t slot, int t) {
+  const int o = t & 15, r = t >> 4;
+  const uint4 s = *reinterpret_cast<const uint4*>(stage + 8192 + 16 * o);
+  const uint4 z = *reinterpret_cast<const uint4*>(stage + 8192 + 256 + 16 * o);
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(stage) + t;
+  const uint32_t at = slot + (o >> 3) * 16384 + r * 128 + (((o & 7) ^ r) << 4);
+  const uint32_t s0 = lo2(s.x, s.z), s1 = hi2(s.x, s.z), s2 = lo2(s.y, s.w), s3 = hi2(s.y, s.w);
+  const uint32_t z0 = lo2(z.x, z.z), z1 = hi2(z.x, z.z), z2 = lo2(z.y, z.w), z3 = hi2(z.y, z.w);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {   // tokens past the group's end count as zero, whatever lies there
-    const int left = valid - 8 * o - 2 * j;
-    const uint32_t m = left >= 2 ? 0xffffffffu : left == 1 ? 0x0000ffffu : 0u;
-    s[j] &= m;
-    z[j] &= m;
+  for (int j = 0; j < 16; ++j) {
+    const uint32_t x = w[128 * j], y = x >> 8;
+    st16(at + 1024 * j, code2<0x000F000Fu, 0x64006400u>(x, s0, z0), code2<0x00F000F0u, 0x54005400u>(x, s1, z1),
+         code2<0x000F000Fu, 0x64006400u>(y, s2, z2), code2<0x00F000F0u, 0x54005400u>(y, s3, z3));
   }
+}
+// A packed group's values: thread t takes word W = t % 16 (eight channels) of the token octets t / 16 and
+// t / 16 + 8.  Tokens past the group's end count as zero, whatever lies there.
+__device__ __forceinline__ void put_values(const uint8_t* stage, uint32_t slot, int t, int valid) {
+  const int W = t & 15;
 #pragma unroll
-  for (int wi = 0; wi < 2; ++wi) {
-    uint32_t w[4], u[4];
+  for (int half = 0; half < 2; ++half) {
+    const int o = (t >> 4) + 8 * half;
+    const uint4 sv = *reinterpret_cast<const uint4*>(stage + 4096 + 16 * o);
+    const uint4 zv = *reinterpret_cast<const uint4*>(stage + 4096 + 256 + 16 * o);
+    uint32_t s[4] = {sv.x, sv.y, sv.z, sv.w}, z[4] = {zv.x, zv.y, zv.z, zv.w}, w[4];
+    const uint32_t* c = reinterpret_cast<const uint32_t*>(stage) + 64 * o + W;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      w[j] = wi ? v.w[j].y : v.w[j].x;
-      u[j] = w[j] >> 8;
+      w[j] = c[16 * j];
+      const int left = valid - 8 * o - 2 * j;
+      const uint32_t m = left >= 2 ? 0xffffffffu : left == 1 ? 0x0000ffffu : 0u;
+      s[j] &= m;
+      z[j] &= m;
     }
+    const uint32_t at = slot + half * 16384 + W * 128 + (((t >> 4) ^ (W & 7)) << 4);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const int r = 16 * (t >> 4) + 8 * wi + c;   // channel
+    for (int e = 0; e < 8; ++e) {
       uint32_t x[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t y = c < 4 ? w[j] : u[j];
-        x[j] = (c & 3) == 0   ? code2<0x00030003u, 0x64006400u>(y, s[j], z[j])
-               : (c & 3) == 1 ? code2<0x000C000Cu, 0x5C005C00u>(y, s[j], z[j])
-               : (c & 3) == 2 ? code2<0x00300030u, 0x54005400u>(y, s[j], z[j])
+        const uint32_t y = e < 4 ? w[j] : w[j] >> 8;
+        x[j] = (e & 3) == 0   ? code2<0x00030003u, 0x64006400u>(y, s[j], z[j])
+               : (e & 3) == 1 ? code2<0x000C000Cu, 0x5C005C00u>(y, s[j], z[j])
+               : (e & 3) == 2 ? code2<0x00300030u, 0x54005400u>(y, s[j], z[j])
                               : code2<0x00C000C0u, 0x4C004C00u>(y, s[j], z[j]);
       }
-      st16(base + r * 128 + (((o & 7) ^ (r & 7)) << 4), x[0], x[1], x[2], x[3]);
+      st16(at + 2048 * e, x[0], x[1], x[2], x[3]);
     }
   }
 }
 
 // Eight channels (octet o) of raw token r of sequence s, head h: the sink's rows, then the window's.
 // What fp16 cannot hold counts as 0 and is flagged.
-__device__ __forceinline__ void raw8(const AttnArgs& a, const Cta& c, int which, int ns, int r, int o, float (&x)[8],
+__device__ __forceinline__ void raw8(const AttnArgs& a, const Seg& c, int which, int ns, int r, int o, float (&x)[8],
                                      int& flags) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) x[j] = 0.0f;
@@ -244,7 +366,7 @@ __device__ __forceinline__ void raw8(const AttnArgs& a, const Cta& c, int which,
     }
   }
 }
-__device__ __forceinline__ int put_raw_k(const AttnArgs& a, const Cta& c, int ns, int r0, uint32_t slot, int t) {
+__device__ __forceinline__ int put_raw_k(const AttnArgs& a, const Seg& c, int ns, int r0, uint32_t slot, int t) {
   int flags = 0;
   const int o = t & 15;
 #pragma unroll 4
@@ -262,7 +384,7 @@ __device__ __forceinline__ int put_raw_k(const AttnArgs& a, const Cta& c, int ns
   }
   return flags;
 }
-__device__ __forceinline__ int put_raw_v(const AttnArgs& a, const Cta& c, int ns, int r0, uint32_t slot, int t) {
+__device__ __forceinline__ int put_raw_v(const AttnArgs& a, const Seg& c, int ns, int r0, uint32_t slot, int t) {
   int flags = 0;
   const int o = t & 15;   // token octet
 #pragma unroll 1
@@ -282,472 +404,672 @@ __device__ __forceinline__ int put_raw_v(const AttnArgs& a, const Cta& c, int ns
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         y[j] = e & 1 ? hi2(h[2 * j][e / 2], h[2 * j + 1][e / 2]) : lo2(h[2 * j][e / 2], h[2 * j + 1][e / 2]);
-      const int r = 8 * ch + e;
+      const int r = 16 * e + ch;   // channel 8 ch + e
       st16(slot + (o >> 3) * 16384 + r * 128 + (((o & 7) ^ (r & 7)) << 4), y[0], y[1], y[2], y[3]);
     }
   }
   return flags;
 }
 
-// The ring's order: position p holds the keys or the values of one tile.
-__device__ __forceinline__ bool is_value(const Cta& c, int p, int* tile) {
-  if (!c.split) {
-    *tile = p >> 1;
-    return p & 1;
-  }
-  if (p == 0) { *tile = 0; return false; }
-  if (p == 2 * c.N - 1) { *tile = c.N - 1; return true; }
-  *tile = p & 1 ? (p + 1) >> 1 : (p >> 1) - 1;
-  return !(p & 1);
+// The ring's order: the position of tile i's keys and of its values, from the block's first on.  Two
+// streams over one tile: K0 V0 K1 V1 ...; over tiles in turn: K0 K1 V0 K2 V1 ..., the last keys being
+// followed by two values.
+__device__ __forceinline__ int ring_k(const Seg& c, int i) { return c.split ? (i == 0 ? 0 : 2 * i - 1) : 2 * i; }
+__device__ __forceinline__ int ring_v(const Seg& c, int i) {
+  return c.split ? (i == c.N - 1 ? 2 * i + 1 : 2 * i + 2) : 2 * i + 1;
 }
 
-__device__ __forceinline__ void producer(const AttnArgs& a, const Cta& c, const AttnSeq& q, Small* sm, uint32_t ring) {
-  const int t = threadIdx.x - 256;
-  const int ns = min(a.b.n_sink, (int)min((int64_t)a.b.n_sink, (int64_t)a.b.n_sink + q.tr + q.tq));
-  int flags = 0;
-  auto slab_of = [&](int tile) -> int64_t {   // packed tile of the block
-    const int g = c.t_lo + tile - c.n_raw;
-    if (g < 0 || tile >= c.N) return 0;
-    int blk = __ldg(a.b.table + (int64_t)c.s * a.b.max_blocks + g);
-    if (blk < 0 || blk >= a.b.num_blocks) {
-      flags |= KVQ_DEV_BOUNDS;
-      blk = 0;
+__device__ __forceinline__ bool seg_wait(Small* sm, int k) {
+  return mbar_wait(smem_u32(&sm->seg_full[k % kSegs]), (k / kSegs) & 1, &sm->stop);
+}
+__device__ __forceinline__ void seg_done(Small* sm, int k, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(smem_u32(&sm->seg_empty[k % kSegs]));
+}
+
+template <bool VALUES>
+__device__ __forceinline__ void producer(const AttnArgs& a, Small* sm, uint32_t ring, const uint8_t* stages) {
+  const int t = threadIdx.x & 127, lane = t & 31;
+  int flags = 0, base = 0, groups = 0;   // ring positions and packed groups before this block
+  bool ok = true;
+  for (int k = 0; ok && (ok = seg_wait(sm, k)); ++k) {
+    const Seg c = sm->seg[k % kSegs];
+    seg_done(sm, k, lane);
+    if (c.N < 0) break;
+    const int ns = (int)min((int64_t)a.b.n_sink, (int64_t)a.b.n_sink + c.tr + c.tq);
+    for (int i = 0; i < c.N; ++i) {
+      const int p = base + (VALUES ? ring_v(c, i) : ring_k(c, i)), slot = p % kSlots, use = p / kSlots;
+      const uint32_t dst = ring + slot * kTile;
+      const int at = c.t_lo + i;
+      if (use > 0 && !(ok = mbar_wait(smem_u32(&sm->empty[slot]), (use - 1) & 1, &sm->stop))) break;
+      if (at < c.n_raw) {
+        flags |= VALUES ? put_raw_v(a, c, ns, 128 * at, dst, t) : put_raw_k(a, c, ns, 128 * at, dst, t);
+        fence_async_smem();
+        mbar_arrive(smem_u32(&sm->full[slot]));
+      } else {
+        const int st = groups % kStages, round = (groups / kStages) & 1;
+        ++groups;
+        if (!(ok = mbar_wait(smem_u32(VALUES ? &sm->v_in[st] : &sm->k_in[st]), round, &sm->stop))) break;
+        const uint8_t* in = stages + st * (kStageK + kStageV) + (VALUES ? kStageK : 0);
+        if (VALUES) put_values(in, dst, t, min(128, c.tq - 128 * (at - c.n_raw)));
+        else put_keys(in, dst, t);
+        fence_async_smem();
+        mbar_arrive(smem_u32(&sm->full[slot]));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(VALUES ? &sm->v_out[st] : &sm->k_out[st]));
+      }
     }
-    return (int64_t)blk * a.L.Hkv + c.h;
-  };
-  KCodes k;
-  VCodes v;
-  // the pages of the next keys and values, one step ahead of their codes
-  const int64_t first = slab_of(0);
-  load_k(a, first, t, k);
-  load_v(a, first, t, v);
-  int64_t next_k = slab_of(1), next_v = next_k;
-  for (int p = 0; p < 2 * c.N; ++p) {
-    const int slot = p % kSlots, use = p / kSlots;
-    int tile;
-    const bool value = is_value(c, p, &tile);
-    if (use > 0 && !mbar_wait(smem_u32(&sm->empty[slot]), (use - 1) & 1, &sm->stop)) break;
-    const uint32_t dst = ring + slot * kTile;
-    const int at = c.t_lo + tile;
-    if (at < c.n_raw) {
-      flags |= value ? put_raw_v(a, c, ns, 128 * at, dst, t) : put_raw_k(a, c, ns, 128 * at, dst, t);
-    } else if (value) {
-      put_v(v, dst, t, min(128, q.tq - 128 * (at - c.n_raw)));
-    } else {
-      put_k(k, dst, t);
-    }
-    fence_async_smem();
-    mbar_arrive(smem_u32(&sm->full[slot]));
-    if (value) {
-      load_v(a, next_v, t, v);
-      next_v = slab_of(tile + 2);
-    } else {
-      load_k(a, next_k, t, k);
-      next_k = slab_of(tile + 2);
-    }
+    base += 2 * c.N;
   }
   flags = __reduce_or_sync(0xffffffffu, flags);
-  if (flags && (t & 31) == 0) flag(a.status, flags);
+  if (flags && lane == 0) flag(a.status, flags);
 }
 
-// ---- the product-issuing thread -----------------------------------------------------------
+// ---- the loader ---------------------------------------------------------------------------------
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void loader(const AttnArgs& a, const Work& work, Small* sm, uint32_t stages, int lane) {
+  const Cut cut = find_cut(a, lane);
+  const int run = blockIdx.x;
+  if (run == 0 && lane == 0) *work.cut = cut;
+  int groups = 0, k = 0, flags = 0;
+  bool ok = true;
+  if (run < cut.runs && cut.units > 0) {
+    int64_t unit, left = run_start(cut, run + 1) - run_start(cut, run);
+    Place p = find_place(a, run_start(cut, run), lane, &unit);
+    for (bool head = true; left > 0 && ok; head = false) {
+      const int tiles = block_tiles(a, p.q, p.b);
+      Seg c;
+      c.row0 = p.q.row0;
+      c.s = p.s;
+      c.h = p.h;
+      c.n = p.q.n;
+      c.tq = p.q.tq;
+      c.tr = p.q.tr;
+      c.r0 = p.b * 256;
+      c.nr = (int)min((int64_t)256, (int64_t)p.q.n * a.G - c.r0);
+      c.split = c.nr <= 128;
+      const Seen last = row_seen(a, p.q, (c.r0 + c.nr - 1) / a.G);
+      c.raw = last.raw;
+      c.packed = last.packed;
+      c.n_raw = (c.raw + 127) / 128;
+      const int64_t end = min((int64_t)tiles + 1, unit + left);
+      c.t_lo = (int)max(unit - 1, (int64_t)0);
+      c.N = (int)max(end - 1 - c.t_lo, (int64_t)0);
+      c.slot = unit <= 1 && end == tiles + 1 ? -1 : 2 * run + (unit <= 1);
+      if (head && lane == 0) {
+        First f;
+        f.row0 = c.row0;
+        f.h = c.h;
+        f.r0 = c.r0;
+        f.nr = c.nr;
+        f.pad = 0;
+        f.unit = unit;
+        f.units = tiles + 1;
+        work.first[run] = f;
+      }
+      left -= end - unit;
+      unit = 0;
+      if (c.N > 0 || tiles == 0) {
+        if (k >= kSegs && !(ok = mbar_wait(smem_u32(&sm->seg_empty[k % kSegs]), (k / kSegs - 1) & 1, &sm->stop))) break;
+        if (lane == 0) {
+          sm->seg[k % kSegs] = c;
+          mbar_arrive(smem_u32(&sm->seg_full[k % kSegs]));
+        }
+        ++k;
+        // the packed groups of this part, pages 32 at a time
+        const int g0 = max(c.t_lo - c.n_raw, 0), g1 = c.t_lo + c.N - c.n_raw;
+        int page = 0;
+        for (int g = g0; g < g1 && ok; ++g) {
+          if (((g - g0) & 31) == 0) {
+            page = g + lane < g1 ? __ldg(a.b.table + (int64_t)c.s * a.b.max_blocks + g + lane) : 0;
+            if (page < 0 || page >= a.b.num_blocks) {
+              flags |= KVQ_DEV_BOUNDS;
+              page = 0;
+            }
+          }
+          const int64_t slab = (int64_t)__shfl_sync(0xffffffffu, page, (g - g0) & 31) * a.L.Hkv + c.h;
+          const int st = groups % kStages, use = groups / kStages;
+          const uint32_t dst = stages + st * (kStageK + kStageV);
+#pragma unroll
+          for (int v = 0; v < 2 && ok; ++v) {
+            const uint32_t out = smem_u32(v ? &sm->v_out[st] : &sm->k_out[st]);
+            const uint32_t in = smem_u32(v ? &sm->v_in[st] : &sm->k_in[st]);
+            if (use > 0) ok = mbar_wait(out, (use - 1) & 1, &sm->stop);
+            if (ok && lane == 0) {
+              const Side& S = a.L.side[v];
+              const uint32_t codes = v ? 4096 : 8192, to = dst + (v ? kStageK : 0);
+              expect_bytes(in, codes + 512);
+              bulk_load(to, reinterpret_cast<const uint8_t*>(S.codes) + slab * S.code_slab_bytes, codes, in);
+              bulk_load(to + codes, reinterpret_cast<const __half*>(S.scale) + slab * 128, 256, in);
+              bulk_load(to + codes + 256, reinterpret_cast<const __half*>(S.zero) + slab * 128, 256, in);
+            }
+          }
+          if (ok) ++groups;
+        }
+      }
+      if (left > 0 && !next_block(a, &p)) break;
+    }
+  }
+  if (ok && (k < kSegs || mbar_wait(smem_u32(&sm->seg_empty[k % kSegs]), (k / kSegs - 1) & 1, &sm->stop))) {
+    if (lane == 0) {
+      sm->seg[k % kSegs].N = -1;
+      mbar_arrive(smem_u32(&sm->seg_full[k % kSegs]));
+    }
+  }
+  if (sm->stop && lane == 0) {   // copies still on their way must land before the memory is given up
+    int never = 0;
+    for (int g = max(groups - kStages, 0); g < groups; ++g) {
+      mbar_wait(smem_u32(&sm->k_in[g % kStages]), (g / kStages) & 1, &never);
+      mbar_wait(smem_u32(&sm->v_in[g % kStages]), (g / kStages) & 1, &never);
+    }
+  }
+  __syncwarp();
+  flags = __reduce_or_sync(0xffffffffu, flags);
+  if (flags && lane == 0) flag(a.status, flags);
+}
+
+// ---- the product-issuing thread -----------------------------------------------------------------
 __device__ __forceinline__ void issue_qk(uint32_t d, uint32_t q, uint32_t k) {
+  const uint64_t dq = smem_desc(q), dk = smem_desc(k);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const uint32_t off = (i >> 2) * 16384 + (i & 3) * 32;
-    mma_ss(d, smem_desc(q + off), smem_desc(k + off), i > 0);
+    const uint64_t off = (i >> 2) * (16384 >> 4) + (i & 3) * 2;
+    mma_ss(d, dq + off, dk + off, i > 0);
   }
 }
 __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t p, uint32_t v, bool accumulate) {
+  const uint64_t dv = smem_desc(v);
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    mma_ts(d, p + 8 * i, smem_desc(v + (i >> 2) * 16384 + (i & 3) * 32), accumulate || i > 0);
+  for (int i = 0; i < 8; ++i) mma_ts(d, p + 8 * i, dv + (i >> 2) * (16384 >> 4) + (i & 3) * 2, accumulate || i > 0);
 }
 
-__device__ __forceinline__ bool products(const Cta& c, Small* sm, uint32_t qs, uint32_t ring, uint32_t tm) {
+__device__ __forceinline__ bool products(Small* sm, uint32_t qs, uint32_t ring, uint32_t tm) {
   volatile int* stop = &sm->stop;
-  int pos = 0;   // ring position consumed next
-  auto slot = [&](int p) { return ring + (p % kSlots) * kTile; };
-  auto full = [&](int p) { return mbar_wait(smem_u32(&sm->full[p % kSlots]), (p / kSlots) & 1, stop); };
-  auto freed = [&](int p) { tc_commit(smem_u32(&sm->empty[p % kSlots])); };
-  auto weights = [&](int w, int i) {
-    const bool ok = mbar_wait(smem_u32(&sm->p_full[w]), i & 1, stop);
+  int base = 0, blocks = 0, np[2] = {0, 0};   // ring positions, blocks and weights of each stream so far
+  auto slot = [&](int p) { return ring + ((base + p) % kSlots) * kTile; };
+  auto full = [&](int p) {
+    const bool ok = mbar_wait(smem_u32(&sm->full[(base + p) % kSlots]), ((base + p) / kSlots) & 1, stop);
     tc_fence_after();
     return ok;
   };
-  if (!c.split) {
-    if (!full(0)) return false;
-    for (int w = 0; w < 2; ++w) {
-      issue_qk(tm + 128 * w, qs + w * kTile, slot(0));
-      tc_commit(smem_u32(&sm->s_full[w]));
-    }
-    freed(0);
-    for (int i = 0; i < c.N; ++i) {
-      const int pv = 2 * i + 1, pk = pv + 1;
-      for (int w = 0; w < 2; ++w) {
-        if (!weights(w, i)) return false;
-        if (w == 0 && !full(pv)) return false;
-        issue_pv(tm + 256 + 128 * w, tm + 128 * w, slot(pv), i > 0);
-        if (w == 1) freed(pv);
-        if (i + 1 < c.N) {
-          if (w == 0 && !full(pk)) return false;
-          issue_qk(tm + 128 * w, qs + w * kTile, slot(pk));
-          tc_commit(smem_u32(&sm->s_full[w]));
-          if (w == 1) freed(pk);
+  auto freed = [&](int p) { tc_commit(smem_u32(&sm->empty[(base + p) % kSlots])); };
+  auto weights = [&](int w) {
+    const bool ok = mbar_wait(smem_u32(&sm->p_full[w]), np[w]++ & 1, stop);
+    tc_fence_after();
+    return ok;
+  };
+  auto scores = [&](int w, int p) {
+    issue_qk(tm + 128 * w, qs + (w ? kTile : 0), slot(p));
+    tc_commit(smem_u32(&sm->s_full[w]));
+  };
+  for (int k = 0;; ++k) {
+    if (!seg_wait(sm, k)) return false;
+    const int N = sm->seg[k % kSegs].N, split = sm->seg[k % kSegs].split;
+    mbar_arrive(smem_u32(&sm->seg_empty[k % kSegs]));
+    if (N < 0) return true;
+    if (N == 0) continue;
+    if (!mbar_wait(smem_u32(&sm->q_full), blocks++ & 1, stop)) return false;
+    tc_fence_after();
+    if (!split) {
+      if (!full(0)) return false;
+      scores(0, 0);
+      scores(1, 0);
+      freed(0);
+      for (int i = 0; i < N; ++i) {
+        const int pv = 2 * i + 1, pk = pv + 1;
+        for (int w = 0; w < 2; ++w) {
+          if (!weights(w)) return false;
+          if (w == 0 && !full(pv)) return false;
+          issue_pv(tm + 256 + 128 * w, tm + 128 * w + 32, slot(pv), i > 0);
+          if (w == 1) freed(pv);
+          if (i + 1 < N) {
+            if (w == 0 && !full(pk)) return false;
+            scores(w, pk);
+            if (w == 1) freed(pk);
+          } else {
+            tc_commit(smem_u32(&sm->o_full[w]));
+          }
+        }
+      }
+    } else {
+      int pos = 0;
+      auto first_scores = [&](int w) {   // both streams have the one Q tile
+        issue_qk(tm + 128 * w, qs, slot(pos));
+        tc_commit(smem_u32(&sm->s_full[w]));
+        freed(pos++);
+      };
+      for (int w = 0; w < 2 && w < N; ++w) {
+        if (!full(pos)) return false;
+        first_scores(w);
+      }
+      for (int t = 0; t < N; ++t) {
+        const int w = t & 1;
+        if (!weights(w) || !full(pos)) return false;
+        issue_pv(tm + 256 + 128 * w, tm + 128 * w + 32, slot(pos), t > 1);
+        freed(pos++);
+        if (t + 2 < N) {
+          if (!full(pos)) return false;
+          first_scores(w);
         } else {
           tc_commit(smem_u32(&sm->o_full[w]));
         }
       }
     }
-    return true;
+    base += 2 * N;
   }
-  for (int w = 0; w < 2 && w < c.N; ++w, ++pos) {
-    if (!full(pos)) return false;
-    issue_qk(tm + 128 * w, qs, slot(pos));
-    tc_commit(smem_u32(&sm->s_full[w]));
-    freed(pos);
-  }
-  for (int t = 0; t < c.N; ++t) {
-    const int w = t & 1;
-    if (!weights(w, t >> 1) || !full(pos)) return false;
-    issue_pv(tm + 256 + 128 * w, tm + 128 * w, slot(pos), t > 1);
-    freed(pos++);
-    if (t + 2 < c.N) {
-      if (!full(pos)) return false;
-      issue_qk(tm + 128 * w, qs, slot(pos));
-      tc_commit(smem_u32(&sm->s_full[w]));
-      freed(pos++);
-    } else {
-      tc_commit(smem_u32(&sm->o_full[w]));
-    }
-  }
-  return true;
 }
 
-// ---- softmax ---------------------------------------------------------------------------------
-__device__ __forceinline__ void pin32(uint32_t* r) {   // orders uses of r after the wait before it
+// ---- softmax --------------------------------------------------------------------------------------
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float* a, float* b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+template <int N>
+__device__ __forceinline__ void pin(uint32_t (&r)[N]) {   // orders uses of r after the wait before it
 #pragma unroll
-  for (int j = 0; j < 32; ++j) asm volatile("" : "+r"(r[j]));
+  for (int j = 0; j < N; ++j) asm volatile("" : "+r"(r[j]));
+}
+__device__ __forceinline__ void chunk_mask(uint32_t (&x)[32], int cols) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (j >= cols) x[j] = 0xff800000u;   // -inf
+}
+__device__ __forceinline__ float chunk_max(const uint32_t (&x)[32]) {
+  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int j = 0; j < 32; j += 8)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m[e] = fmaxf(fmaxf(m[e], __uint_as_float(x[j + e])), __uint_as_float(x[j + e + 4]));
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+// 32 scores to weights 2^(score * cs + off): their sum in fp32, themselves as fp16 to 16 columns.
+__device__ __forceinline__ void chunk_weights(const uint32_t (&x)[32], uint64_t cs2, uint64_t off2, uint64_t* sum0,
+                                              uint64_t* sum1, uint32_t to) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    uint32_t h[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int j = 8 * k + e;
+      float p0, p1;
+      unpair(fma2(pair(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), cs2, off2), &p0, &p1);
+      p0 = exp2_approx(p0);
+      p1 = exp2_approx(p1);
+      uint64_t* sum = j & 1 ? sum1 : sum0;
+      *sum = add2(*sum, pair(p0, p1));
+      h[e] = pack_f16(p0, p1);
+    }
+    tmem_st8(to + 8 * k, h);
+  }
 }
 
-// Stream w's tiles; row of this thread: m (log2), l on return.
-__device__ __forceinline__ bool softmax(const Cta& c, Small* sm, uint32_t s_col, uint32_t o_col, int w, Seen see,
-                                        float cs, float* m_out, float* l_out) {
-  float m = -INFINITY, l = 0.0f;
-  const int n = c.split ? (c.N - w + 1) / 2 : c.N;
-  bool ok = true;
-  for (int i = 0; i < n; ++i) {
-    if (!mbar_wait(smem_u32(&sm->s_full[w]), i & 1, &sm->stop)) { ok = false; break; }
-    tc_fence_after();
-    uint32_t x[128];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) tmem_ld32(s_col + 32 * k, x + 32 * k);
-    tmem_wait_ld();
-#pragma unroll
-    for (int k = 0; k < 4; ++k) pin32(x + 32 * k);
-    const int at = c.t_lo + (c.split ? 2 * i + w : i);
-    const int cols = at < c.n_raw ? see.raw - 128 * at : see.packed - 128 * (at - c.n_raw);
-    if (__any_sync(0xffffffffu, cols < 128)) {
-#pragma unroll
-      for (int j = 0; j < 128; ++j)
-        if (j >= cols) x[j] = 0xff800000u;   // -inf
-    }
-    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-    for (int j = 0; j < 128; j += 4)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(x[j + e]));
-    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs;
-    const bool move = top > m + kLazy;       // true from -inf for any finite score
-    if (__any_sync(0xffffffffu, move)) {
-      const float mn = move ? top : m;
-      const float f = move ? exp2_approx(m - mn) : 1.0f;
-      l *= f;
-      m = mn;
-      if (i > 0) {
+// The queries of 128 rows (tile w) by `warps` warps: a warp per row, four channels per lane, four
+// rows at a time; scaled so that the row's largest lies in [2^8, 2^9).
+__device__ __forceinline__ bool stage_queries(const AttnArgs& a, const Seg& c, Small* sm, uint32_t qs, int w, int wi,
+                                              int warps, int lane) {
+  bool bad = false;
 #pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
-          uint32_t o[32];
-          tmem_ld32(o_col + 32 * k, o);
-          tmem_wait_ld();
-          pin32(o);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-          tmem_st32(o_col + 32 * k, o);
-        }
-      }
-    }
-    const float off = kLift - (m == -INFINITY ? 0.0f : m);
-    float sum[4] = {0, 0, 0, 0};
+  for (int rb = 128 * w + wi; rb < 128 * w + 128; rb += 4 * warps) {
+    uint4 v[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      uint32_t h[16];
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const float p0 = exp2_approx(fmaf(__uint_as_float(x[32 * k + 2 * j]), cs, off));
-        const float p1 = exp2_approx(fmaf(__uint_as_float(x[32 * k + 2 * j + 1]), cs, off));
-        sum[(2 * j) & 3] += p0;
-        sum[(2 * j + 1) & 3] += p1;
-        h[j] = pack_f16(p0, p1);
-      }
-      tmem_st16(s_col + 16 * k, h);
-    }
-    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-    tmem_wait_st();
-    tc_fence_before();
-    mbar_arrive(smem_u32(&sm->p_full[w]));
-  }
-  *m_out = m;
-  *l_out = l;
-  return ok;
-}
-
-struct Plan {
-  int splits;       // runs of tiles of a block (grid z), each `tiles` long
-  int tiles;
-  int64_t rows;     // n_rows * Hq
-  float* m;         // [splits][rows], for splits > 1
-  float* l;
-  float* o;         // [splits][rows][128]
-};
-
-// One row's state to where it goes: the output, or the slot of this run of tiles.
-__device__ __forceinline__ void put_state(const AttnArgs& a, const Plan& p, int64_t row, int z, float m, float l) {
-  if (p.splits > 1) {
-    p.m[z * p.rows + row] = m;
-    p.l[z * p.rows + row] = l;
-  } else if (a.lse) {
-    a.lse[row] = l > 0.0f ? kLn2 * (m + log2f(l) - kLift) : -INFINITY;
-  }
-}
-__device__ __forceinline__ void put_out(const AttnArgs& a, const Plan& p, int64_t row, int z, int c0, const float* x,
-                                        float inv) {
-  if (p.splits > 1) {
-    float4* d = reinterpret_cast<float4*>(p.o + (z * p.rows + row) * 128 + c0);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) d[j] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
-  } else if (a.out_dtype == KVQ_F32) {
-    float4* d = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + row * 128 + c0);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      d[j] = make_float4(x[4 * j] * inv, x[4 * j + 1] * inv, x[4 * j + 2] * inv, x[4 * j + 3] * inv);
-  } else {
-    uint4* d = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + row * 128 + c0);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t h[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float u = x[8 * j + 2 * e] * inv, v = x[8 * j + 2 * e + 1] * inv;
-        if (a.out_dtype == KVQ_F16) {
-          h[e] = pack_f16(u, v);
+      const int r = rb + k * warps;
+      v[k] = make_uint4(0, 0, 0, 0);
+      if (r < c.nr) {
+        const int64_t e = ((c.row0 + (c.r0 + r) / a.G) * a.Hq + c.h * a.G + (c.r0 + r) % a.G) * 128 + 4 * lane;
+        if (a.q_dtype == KVQ_F32) {
+          v[k] = *reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(a.q) + e);
         } else {
-          const __nv_bfloat162 b2 = __floats2bfloat162_rn(u, v);
-          h[e] = *reinterpret_cast<const uint32_t*>(&b2);
+          const uint2 u = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(a.q) + e);
+          v[k].x = u.x;
+          v[k].y = u.y;
         }
       }
-      d[j] = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = rb + k * warps;
+      float x[4];
+      if (a.q_dtype == KVQ_F32) {
+        x[0] = __uint_as_float(v[k].x); x[1] = __uint_as_float(v[k].y);
+        x[2] = __uint_as_float(v[k].z); x[3] = __uint_as_float(v[k].w);
+      } else if (a.q_dtype == KVQ_F16) {
+        x[0] = half_bits_to_float((uint16_t)(v[k].x & 0xffffu)); x[1] = half_bits_to_float((uint16_t)(v[k].x >> 16));
+        x[2] = half_bits_to_float((uint16_t)(v[k].y & 0xffffu)); x[3] = half_bits_to_float((uint16_t)(v[k].y >> 16));
+      } else {
+        x[0] = __uint_as_float(v[k].x << 16); x[1] = __uint_as_float(v[k].x & 0xffff0000u);
+        x[2] = __uint_as_float(v[k].y << 16); x[3] = __uint_as_float(v[k].y & 0xffff0000u);
+      }
+      bad |= !(isfinite(x[0]) && isfinite(x[1]) && isfinite(x[2]) && isfinite(x[3]));
+      if (a.L.k_rotate) {
+        wht128_quad_unscaled(x, lane);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] *= a.L.rot_scale;
+      }
+      const float top = warp_max(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
+      // 2^(e - 127) <= top < 2^(e - 126); zero, subnormal or overflowing rows get the nearest e that serves
+      const int e = min(max((int)(__float_as_uint(top) >> 23), 10), 250);
+      const float up = __uint_as_float((uint32_t)(262 - e) << 23);   // 2^(8 - (e - 127))
+      if (lane == 0) sm->rowscale[r] = __uint_as_float((uint32_t)(e - 8) << 23);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] *= up;
+      const bool odd = lane & 1;
+      const float y0 = __shfl_xor_sync(0xffffffffu, odd ? x[0] : x[2], 1);
+      const float y1 = __shfl_xor_sync(0xffffffffu, odd ? x[1] : x[3], 1);
+      const uint32_t h0 = odd ? pack_f16(y0, x[2]) : pack_f16(x[0], y0);
+      const uint32_t h1 = odd ? pack_f16(y1, x[3]) : pack_f16(x[1], y1);
+      const int o = lane >> 1;
+      const uint32_t at = qs + w * kTile + (o >> 3) * 16384 + (r & 127) * 128 + (((o & 7) ^ (r & 7)) << 4) + 8 * odd;
+      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(h0), "r"(h1) : "memory");
     }
   }
+  return bad;
 }
 
-template <uint32_t N>
-__device__ __forceinline__ void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <uint32_t N>
-__device__ __forceinline__ void regs_fewer() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-
-// Grid (row blocks of all sequences, KV heads, runs of tiles).
-__global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnArgs a,
-                                                              const __grid_constant__ Plan plan) {
-  extern __shared__ __align__(1024) uint8_t smem[];
-  Small* sm = reinterpret_cast<Small*>(smem + kSmallAt);
-  griddep_wait();
-  griddep_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Cta c;
-  int unit;
-  if (!find_unit(a.b.num_seqs, blockIdx.x, [&](int s) { return attn_blocks(a, s); }, &c.s, &unit)) return;
-  const AttnSeq q = attn_seq(a, c.s);
-  if (!q.ok) {
-    if (blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) flag(a.status, KVQ_DEV_BOUNDS);
+// Eight channels of a row, to the output or to a partial slot.
+__device__ __forceinline__ void put8(const AttnArgs& a, const Work& work, const Seg& c, int64_t row, int r, int ch,
+                                     const float (&x)[8], float inv) {
+  if (c.slot >= 0) {
+    float4* d = reinterpret_cast<float4*>(work.o + ((int64_t)c.slot * work.rows + r) * 128 + ch);
+    d[0] = make_float4(x[0], x[1], x[2], x[3]);
+    d[1] = make_float4(x[4], x[5], x[6], x[7]);
     return;
   }
-  c.h = blockIdx.y;
-  const int64_t all = (int64_t)q.n * a.G;
-  unit = (int)((all + 255) / 256) - 1 - unit;     // blocks that see the most go first
-  c.r0 = unit * 256;
-  c.nr = (int)min((int64_t)256, all - c.r0);
-  c.split = c.nr <= 128;
-  const Seen last = row_seen(a, q, (c.r0 + c.nr - 1) / a.G);
-  c.raw = last.raw;
-  c.packed = last.packed;
-  c.n_raw = (c.raw + 127) / 128;
-  const int tiles = c.n_raw + (c.packed + 127) / 128;
-  c.t_lo = blockIdx.z * plan.tiles;
-  c.N = min(tiles, c.t_lo + plan.tiles) - c.t_lo;
-  // row r of the block: token r / G of the chunk, query head h G + r % G
-  auto out_row = [&](int r) { return (q.row0 + (c.r0 + r) / a.G) * a.Hq + c.h * a.G + (c.r0 + r) % a.G; };
-  if (c.N <= 0) {   // nothing here to see
-    if (plan.splits > 1 || tiles == 0) {
-      for (int r = threadIdx.x; r < c.nr; r += kThreads) {
-        const int64_t row = out_row(r);
-        put_state(a, plan, row, blockIdx.z, -INFINITY, 0.0f);
-        if (plan.splits == 1) {
-          const float zero[32] = {};
-          for (int k = 0; k < 4; ++k) put_out(a, plan, row, 0, 32 * k, zero, 0.0f);
-        }
-      }
-    }
+  if (a.out_dtype == KVQ_F32) {
+    float4* d = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + row * 128 + ch);
+    d[0] = make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+    d[1] = make_float4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv);
     return;
   }
-
-  const uint32_t qs = smem_u32(smem), ring = qs + kSlotsAt;
-  if (warp == 12) tmem_alloc(smem_u32(&sm->tmem), 512);
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(smem_u32(&sm->full[i]), 128);
-      mbar_init(smem_u32(&sm->empty[i]), 1);
-    }
-    for (int w = 0; w < 2; ++w) {
-      mbar_init(smem_u32(&sm->s_full[w]), 1);
-      mbar_init(smem_u32(&sm->p_full[w]), 128);
-      mbar_init(smem_u32(&sm->o_full[w]), 1);
-    }
-    mbar_init(smem_u32(&sm->drain), 1);
-    sm->stop = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  // queries: a warp per row, four channels per lane; scaled so that the row's largest lies in [2^8, 2^9)
-  bool bad = false;
-  for (int r = warp; r < (c.split ? 128 : 256); r += kThreads / 32) {
-    float x[4] = {0, 0, 0, 0};
-    if (r < c.nr) {
-      const int64_t e = out_row(r) * 128 + 4 * lane;
-      if (a.q_dtype == KVQ_F32) {
-        const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.q) + e);
-        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-      } else {
-        const uint2 v = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(a.q) + e);
-        const uint32_t w[2] = {v.x, v.y};
+  uint32_t h[4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if (a.q_dtype == KVQ_F16) {
-            x[2 * j] = half_bits_to_float((uint16_t)(w[j] & 0xffffu));
-            x[2 * j + 1] = half_bits_to_float((uint16_t)(w[j] >> 16));
-          } else {
-            x[2 * j] = __uint_as_float(w[j] << 16);
-            x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+  for (int e = 0; e < 4; ++e) {
+    const float u = x[2 * e] * inv, v = x[2 * e + 1] * inv;
+    if (a.out_dtype == KVQ_F16) {
+      h[e] = pack_f16(u, v);
+    } else {
+      const __nv_bfloat162 b2 = __floats2bfloat162_rn(u, v);
+      h[e] = *reinterpret_cast<const uint32_t*>(&b2);
+    }
+  }
+  *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + row * 128 + ch) = make_uint4(h[0], h[1], h[2], h[3]);
+}
+
+__device__ __forceinline__ void softmax_warp(const AttnArgs& a, const Work& work, Small* sm, uint8_t* smem, uint32_t qs,
+                                             uint32_t tm, int warp, int lane) {
+  const int w = warp >> 3, hf = (warp >> 2) & 1, row = 32 * (warp & 3) + lane;   // stream, half, row of its tile
+  const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // lane 32 (warp % 4) in the address's upper half
+  const uint32_t s_col = tm + lanes + 128 * w, o_col = tm + lanes + 256 + 128 * w;
+  // the half's two chunks: the one read twice, and the one kept, whose columns take the weights
+  const uint32_t far = s_col + (hf ? 96 : 0), near = s_col + (hf ? 64 : 32);
+  const int far_at = hf ? 96 : 0, near_at = hf ? 64 : 32;
+  const uint32_t far_to = s_col + 32 + far_at / 2, near_to = s_col + 32 + near_at / 2;
+  volatile int* stop = &sm->stop;
+  auto sync2 = [&](uint64_t* bar, int* count) {   // a barrier of counted warps
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(bar));
+    return mbar_wait(smem_u32(bar), (*count)++ & 1, stop);
+  };
+  int ns = 0, no = 0, n_rows = 0, n_quads = 0, n_all = 0, blocks = 0;   // phases of the barriers waited on
+  for (int k = 0;; ++k) {
+    if (!seg_wait(sm, k)) return;
+    const Seg c = sm->seg[k % kSegs];
+    if (c.N < 0) return;
+    const int r = c.split ? row : 128 * w + row;
+    const int64_t out_row = (c.row0 + (c.r0 + r) / a.G) * a.Hq + c.h * a.G + (c.r0 + r) % a.G;
+    if (c.N == 0) {   // no token for any row
+      if (r < c.nr && !(c.split && w)) {
+        const float zero[8] = {};
+        for (int i = 0; i < 8; ++i) put8(a, work, c, out_row, r, 64 * hf + 8 * i, zero, 0.0f);
+        if (a.lse && hf == 0) a.lse[out_row] = -INFINITY;
+      }
+      seg_done(sm, k, lane);
+      continue;
+    }
+    bool bad = false;
+    if (!c.split) bad = stage_queries(a, c, sm, qs, w, warp & 7, 8, lane);
+    else bad = stage_queries(a, c, sm, qs, 0, warp, 16, lane);
+    if (__any_sync(0xffffffffu, bad) && lane == 0) flag(a.status, KVQ_DEV_NONFINITE);
+    fence_async_smem();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sm->q_full));
+    if (!sync2(&sm->all, &n_all)) return;   // row scales
+
+    Seen see = {0, 0};
+    if (r < c.nr) {
+      AttnSeq q;
+      q.n = c.n;
+      q.tq = c.tq;
+      q.tr = c.tr;
+      see = row_seen(a, q, (c.r0 + r) / a.G);
+    }
+    const bool live = (r & ~31) < c.nr;      // a row of this warp is real
+    // never 0, so that a masked score of -inf stays one
+    const float cs = fmaxf(a.qscale * sm->rowscale[r], 1.2e-38f);
+    float m = -INFINITY, l = 0.0f;
+    const int n = c.split ? (c.N - w + 1) / 2 : c.N;
+    for (int i = 0; i < n; ++i) {
+      if (!mbar_wait(smem_u32(&sm->s_full[w]), ns++ & 1, stop)) return;
+      if (!live) {   // these weights are never read
+        if (lane == 0) mbar_arrive(smem_u32(&sm->p_full[w]));
+        continue;
+      }
+      tc_fence_after();
+      const int at = c.t_lo + (c.split ? 2 * i + w : i);
+      const int cols = at < c.n_raw ? see.raw - 128 * at : see.packed - 128 * (at - c.n_raw);
+      const bool edge = __any_sync(0xffffffffu, cols < 128);
+      uint32_t x[32];
+      tmem_ld32(far, x);
+      tmem_wait_ld();
+      pin(x);
+      if (edge) chunk_mask(x, cols - far_at);
+      float top = chunk_max(x);
+      tmem_ld32(near, x);
+      tmem_wait_ld();
+      pin(x);
+      if (edge) chunk_mask(x, cols - near_at);
+      top = fmaxf(top, chunk_max(x));
+      sm->mx[w][hf][row] = top;
+      if (!sync2(&sm->row_pair[4 * w + (warp & 3)], &n_rows)) return;
+      top = fmaxf(top, sm->mx[w][hf ^ 1][row]) * cs;
+      const bool move = top > m + kLazy;     // true from -inf for any finite score
+      if (__any_sync(0xffffffffu, move)) {
+        const float mn = move ? top : m;
+        const float f = move ? exp2_approx(m - mn) : 1.0f;
+        l *= f;
+        m = mn;
+        if (i > 0) {   // this half's columns of O; rare: few registers rather than few loads
+#pragma unroll 1
+          for (int e = 0; e < 8; ++e) {
+            uint32_t o[8];
+            tmem_ld8(o_col + 64 * hf + 8 * e, o);
+            tmem_wait_ld();
+            pin(o);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+            tmem_st8(o_col + 64 * hf + 8 * e, o);
           }
         }
       }
+      const float off = kLift - (m == -INFINITY ? 0.0f : m);
+      const uint64_t cs2 = pair(cs, cs), off2 = pair(off, off);
+      uint64_t sum0 = 0, sum1 = 0;
+      chunk_weights(x, cs2, off2, &sum0, &sum1, near_to);
+      tmem_ld32(far, x);
+      tmem_wait_ld();
+      pin(x);
+      if (edge) chunk_mask(x, cols - far_at);
+      chunk_weights(x, cs2, off2, &sum0, &sum1, far_to);
+      float e0, e1;
+      unpair(add2(sum0, sum1), &e0, &e1);
+      l += e0 + e1;
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm->p_full[w]));
     }
-    bad |= !(isfinite(x[0]) && isfinite(x[1]) && isfinite(x[2]) && isfinite(x[3]));
-    if (a.L.k_rotate) {
-      wht128_quad_unscaled(x, lane);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] *= a.L.rot_scale;
-    }
-    const float top = warp_max(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
-    // 2^e <= top < 2^(e + 1); rows of zeros, subnormal or overflowing rows get the nearest e that serves
-    const int e = min(max((int)(__float_as_uint(top) >> 23), 10), 250);
-    const float up = __uint_as_float((uint32_t)(262 - e) << 23);   // 2^(8 - (e - 127))
-    if (lane == 0) sm->rowscale[r] = __uint_as_float((uint32_t)(e - 8) << 23);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] *= up;
-    const bool odd = lane & 1;
-    const float y0 = __shfl_xor_sync(0xffffffffu, odd ? x[0] : x[2], 1);
-    const float y1 = __shfl_xor_sync(0xffffffffu, odd ? x[1] : x[3], 1);
-    const uint32_t h0 = odd ? pack_f16(y0, x[2]) : pack_f16(x[0], y0);
-    const uint32_t h1 = odd ? pack_f16(y1, x[3]) : pack_f16(x[1], y1);
-    const int o = lane >> 1;
-    const uint32_t at = qs + (r >> 7) * kTile + (o >> 3) * 16384 + (r & 127) * 128 + (((o & 7) ^ (r & 7)) << 4) + 8 * odd;
-    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(h0), "r"(h1) : "memory");
-  }
-  if (__any_sync(0xffffffffu, bad) && lane == 0) flag(a.status, KVQ_DEV_NONFINITE);
-  fence_async_smem();
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tm = sm->tmem;
 
-  if (warp < 8) {
-    regs_more<184>();
-    const int w = warp >> 2, t = threadIdx.x & 127;
-    const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // lane 32 (warp % 4) in the address's upper half
-    const int r = c.split ? t : 128 * w + t;
-    Seen see = {0, 0};
-    if (r < c.nr) see = row_seen(a, q, (c.r0 + r) / a.G);
-    // never 0, so that a masked score of -inf stays one
-    const float cs = fmaxf(a.qscale * sm->rowscale[r], 1.2e-38f);
-    const uint32_t o_col = tm + lanes + 256 + 128 * w;
-    float m, l;
-    bool ok = softmax(c, sm, tm + lanes + 128 * w, o_col, w, see, cs, &m, &l);
-    const bool two = c.split && c.N > 1;                  // two states per row to merge
-    if (ok && (w == 0 || c.N > 1 || !c.split)) ok = mbar_wait(smem_u32(&sm->o_full[w]), 0, &sm->stop);
-    if (two && w == 1) {
-      // the other stream's products may still read the ring
-      if (ok) ok = mbar_wait(smem_u32(&sm->o_full[0]), 0, &sm->stop);
-      tc_fence_after();
-      if (ok) {
-        sm->m1[t] = m;
-        sm->l1[t] = l;
-        float4* d = reinterpret_cast<float4*>(smem + kSlotsAt) + t * 32;
+    // the state of stream w's rows: l over both halves, then over both streams of a split block
+    const bool two = c.split && c.N > 1;
+    if (n > 0 && !mbar_wait(smem_u32(&sm->o_full[w]), no++ & 1, stop)) return;
+    // stream 1 is to write over Q, which the other stream's products may still read
+    if (two && w == 1 && !mbar_wait(smem_u32(&sm->o_full[0]), blocks & 1, stop)) return;
+    ++blocks;
+    tc_fence_after();
+    if (n > 0) {
+      if (!sync2(&sm->row_pair[4 * w + (warp & 3)], &n_rows)) return;   // mx has been read
+      sm->mx[w][hf][row] = l;
+      if (!sync2(&sm->row_pair[4 * w + (warp & 3)], &n_rows)) return;
+      l += sm->mx[w][hf ^ 1][row];
+    }
+    float f0 = 1.0f, f1 = 0.0f;
+    float4* other = reinterpret_cast<float4*>(smem) + (hf * 128 + row) * 16;   // 64 floats of this row, over Q
+    if (two) {
+      if (w == 1) {
+        sm->m1[row] = m;
+        sm->l1[row] = l;
 #pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
-          uint32_t o[32];
-          tmem_ld32(o_col + 32 * k, o);
+        for (int e = 0; e < 8; ++e) {
+          uint32_t o[8];
+          tmem_ld8(o_col + 64 * hf + 8 * e, o);
           tmem_wait_ld();
-          pin32(o);
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            d[(8 * k + j) ^ lane] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]),
-                                                __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
+          pin(o);
+          other[(2 * e) ^ (lane & 15)] = make_float4(__uint_as_float(o[0]), __uint_as_float(o[1]), __uint_as_float(o[2]),
+                                                     __uint_as_float(o[3]));
+          other[(2 * e + 1) ^ (lane & 15)] = make_float4(__uint_as_float(o[4]), __uint_as_float(o[5]),
+                                                         __uint_as_float(o[6]), __uint_as_float(o[7]));
         }
       }
-    }
-    if (two) asm volatile("bar.sync 1, 256;" ::: "memory");
-    if (ok && (w == 0 || !c.split)) {
-      tc_fence_after();
-      float f0 = 1.0f, f1 = 0.0f;
-      if (two) {
-        const float m1 = sm->m1[t], l1 = sm->l1[t], mm = fmaxf(m, m1);
+      if (!sync2(&sm->row_quad[warp & 3], &n_quads)) return;
+      if (w == 0) {
+        const float m1 = sm->m1[row], l1 = sm->l1[row], mm = fmaxf(m, m1);
         f0 = m == -INFINITY ? 0.0f : exp2_approx(m - mm);
         f1 = m1 == -INFINITY ? 0.0f : exp2_approx(m1 - mm);
         l = l * f0 + l1 * f1;
         m = mm;
       }
+    }
+    if (w == 0 || !c.split) {
       const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-      const int64_t row = r < c.nr ? out_row(r) : 0;
-      if (r < c.nr) put_state(a, plan, row, blockIdx.z, m, l);
-      const float4* d = reinterpret_cast<const float4*>(smem + kSlotsAt) + t * 32;
-#pragma unroll 1
-      for (int k = 0; k < 4; ++k) {
-        uint32_t o[32];
-        float x[32];
-        tmem_ld32(o_col + 32 * k, o);
-        tmem_wait_ld();
-        pin32(o);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(o[j]);
-        if (two) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float4 v = d[(8 * k + j) ^ lane];
-            x[4 * j] = x[4 * j] * f0 + v.x * f1;
-            x[4 * j + 1] = x[4 * j + 1] * f0 + v.y * f1;
-            x[4 * j + 2] = x[4 * j + 2] * f0 + v.z * f1;
-            x[4 * j + 3] = x[4 * j + 3] * f0 + v.w * f1;
-          }
+      if (r < c.nr && hf == 0) {
+        if (c.slot >= 0) {
+          work.m[(int64_t)c.slot * work.rows + r] = m;
+          work.l[(int64_t)c.slot * work.rows + r] = l;
+        } else if (a.lse) {
+          a.lse[out_row] = l > 0.0f ? kLn2 * (m + log2f(l) - kLift) : -INFINITY;
         }
-        if (r < c.nr) put_out(a, plan, row, blockIdx.z, 32 * k, x, inv);
+      }
+      // columns 16 c + W hold channel 8 W + c: eight loads of four columns give four octets, W = 4 i ..; this
+      // half of the threads takes W = 8 hf .. 8 hf + 7
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i) {
+        uint32_t o[8][4];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) tmem_ld4(o_col + 16 * e + 8 * hf + 4 * i, o[e]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) pin(o[e]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(o[e][j]);
+          if (two) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {   // column 16 e + W of the other stream
+              const int col = 16 * e + 8 * hf + 4 * i + j;
+              const float* y = reinterpret_cast<const float*>(reinterpret_cast<float4*>(smem) +
+                                                              ((col >> 6) * 128 + row) * 16 +
+                                                              (((col & 63) >> 2) ^ (lane & 15)));
+              x[e] = x[e] * f0 + y[col & 3] * f1;
+            }
+          }
+          if (r < c.nr) put8(a, work, c, out_row, r, 8 * (8 * hf + 4 * i + j), x, inv);
+        }
       }
     }
-  } else if (warp < 12) {
-    regs_fewer<104>();
-    producer(a, c, q, sm, ring);
-  } else {
-    regs_fewer<40>();
-    if (warp == 12 && lane == 0 && !products(c, sm, qs, ring, tm)) {
+    tc_fence_before();
+    seg_done(sm, k, lane);
+    if (!sync2(&sm->all, &n_all)) return;   // Q and the states may be overwritten
+  }
+}
+
+// One CTA per SM, each with its run of units.
+__global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnArgs a,
+                                                              const __grid_constant__ Work work) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Small* sm = reinterpret_cast<Small*>(smem + kSmallAt);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t qs = smem_u32(smem), ring = qs + kSlotsAt;
+  if (threadIdx.x == 0) {
+    auto init = [](uint64_t& b, uint32_t n) { mbar_init(smem_u32(&b), n); };
+    for (int i = 0; i < kSlots; ++i) {
+      init(sm->full[i], 128);
+      init(sm->empty[i], 1);
+    }
+    for (int i = 0; i < kStages; ++i) {
+      init(sm->k_in[i], 1);
+      init(sm->v_in[i], 1);
+      init(sm->k_out[i], 4);
+      init(sm->v_out[i], 4);
+    }
+    for (int i = 0; i < kSegs; ++i) {
+      init(sm->seg_full[i], 1);
+      init(sm->seg_empty[i], 25);   // softmax and producer warps, the product thread
+    }
+    for (int w = 0; w < 2; ++w) {
+      init(sm->s_full[w], 1);
+      init(sm->p_full[w], 8);
+      init(sm->o_full[w], 1);
+    }
+    for (int i = 0; i < 8; ++i) {
+      init(sm->row_pair[i], 2);
+      if (i < 4) init(sm->row_quad[i], 4);
+    }
+    init(sm->q_full, 16);
+    init(sm->all, 16);
+    init(sm->drain, 1);
+    sm->stop = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  if (warp == 24) tmem_alloc(smem_u32(&sm->tmem), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = sm->tmem;
+  if (warp < 16) {
+    softmax_warp(a, work, sm, smem, qs, tm, warp, lane);
+  } else if (warp < 20) {
+    producer<false>(a, sm, ring, smem + kStagesAt);
+  } else if (warp < 24) {
+    producer<true>(a, sm, ring, smem + kStagesAt);
+  } else if (warp == 24) {
+    if (lane == 0 && !products(sm, qs, ring, tm)) {
       // stopped: what was issued still has to end before its memory is given up
       flag(a.status, KVQ_DEV_TIMEOUT);
       tc_commit(smem_u32(&sm->drain));
@@ -755,39 +1077,47 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       mbar_wait(smem_u32(&sm->drain), 0, &never);
     }
     __syncwarp();
+  } else {
+    loader(a, work, sm, qs + kStagesAt, lane);
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) tmem_free(tm, 512);
+  if (warp == 24) tmem_free(tm, 512);
 }
 
-// Merge of the runs of tiles: a warp per row, four channels per lane.
+// Run i's CTA merges the block that run i continues if run i - 1 began it: that run's last slot, then
+// the first slots of run i and of those after it that still belong to the block.  A warp per row, four
+// channels per lane.
 __global__ void __launch_bounds__(256) attn_merge_kernel(const __grid_constant__ AttnArgs a,
-                                                         const __grid_constant__ Plan plan) {
+                                                         const __grid_constant__ Work work) {
   griddep_wait();
   griddep_launch_dependents();
-  int s, unit;
-  if (!find_unit(a.b.num_seqs, blockIdx.x, [&](int i) { return attn_blocks(a, i); }, &s, &unit)) return;
-  const AttnSeq q = attn_seq(a, s);
-  if (!q.ok) return;
+  const Cut cut = *work.cut;
+  const int run = blockIdx.x + 1;
+  if (run >= cut.runs) return;
+  const First f = work.first[run];
+  const int64_t lo = run_start(cut, run), prev = run_start(cut, run - 1);
+  if (f.unit < 2 || f.unit - (lo - prev) > 1) return;
+  const int64_t end = lo - f.unit + f.units;   // where the block ends
+  int parts = 2;
+  while (run + parts - 1 < cut.runs && run_start(cut, run + parts - 1) < end) ++parts;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t all = (int64_t)q.n * a.G;
-  for (int64_t r = unit * 256 + warp; r < min(all, (int64_t)unit * 256 + 256); r += 8) {
-    const int64_t row = (q.row0 + r / a.G) * a.Hq + blockIdx.y * a.G + r % a.G;
+  auto slot = [&](int z) { return (int64_t)(z == 0 ? 2 * run - 1 : 2 * (run + z - 1)) * work.rows; };
+  for (int r = warp + 8 * blockIdx.y; r < f.nr; r += 8 * gridDim.y) {
+    const int64_t row = (f.row0 + (f.r0 + r) / a.G) * a.Hq + f.h * a.G + (f.r0 + r) % a.G;
     float m = -INFINITY;
-    for (int z = lane; z < plan.splits; z += 32) m = fmaxf(m, plan.m[z * plan.rows + row]);
-    m = warp_max(m);
+    for (int z = 0; z < parts; ++z) m = fmaxf(m, work.m[slot(z) + r]);
     float l = 0.0f, o[4] = {0, 0, 0, 0};
-    for (int z = 0; z < plan.splits; ++z) {
-      const float mz = plan.m[z * plan.rows + row];
+    for (int z = 0; z < parts; ++z) {
+      const float mz = work.m[slot(z) + r];
       if (mz == -INFINITY) continue;
-      const float f = exp2_approx(mz - m);
-      l += f * plan.l[z * plan.rows + row];
-      const float4 v = *reinterpret_cast<const float4*>(plan.o + (z * plan.rows + row) * 128 + 4 * lane);
-      o[0] += f * v.x;
-      o[1] += f * v.y;
-      o[2] += f * v.z;
-      o[3] += f * v.w;
+      const float g = exp2_approx(mz - m);
+      l += g * work.l[slot(z) + r];
+      const float4 v = *reinterpret_cast<const float4*>(work.o + (slot(z) + r) * 128 + 4 * lane);
+      o[0] += g * v.x;
+      o[1] += g * v.y;
+      o[2] += g * v.z;
+      o[3] += g * v.w;
     }
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
@@ -796,53 +1126,38 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const __grid_constant__
   }
 }
 
-int64_t row_blocks(int num_seqs, int G, int64_t n_rows) { return n_rows * G / 256 + num_seqs; }
-
-// Runs of tiles: enough CTAs for two per SM when the row blocks alone do not give them, at least four
-// tiles each.
-Plan make_plan(int num_seqs, int Hq, int Hkv, int64_t n_rows, int64_t max_new, int64_t max_tq, int max_tr, int ns) {
-  const int G = Hq / Hkv;
-  const int64_t per_seq = (max_new * G + 255) / 256;
-  const int64_t blocks = row_blocks(num_seqs, G, n_rows) < per_seq * num_seqs ? row_blocks(num_seqs, G, n_rows)
-                                                                              : per_seq * num_seqs;
-  const int64_t ctas = blocks * Hkv, tiles = (max_tq + 127) / 128 + (ns + max_tr + 127) / 128;
-  const int64_t want = 2 * device_sm_count();
-  Plan p = {};
-  p.rows = n_rows * Hq;
-  p.tiles = (int)tiles;
-  if (ctas < want) {
-    const int64_t t = (ctas * tiles + want - 1) / want;
-    p.tiles = (int)(t < 4 ? 4 : t);
-  }
-  if (p.tiles < 1) p.tiles = 1;
-  p.splits = (int)((tiles + p.tiles - 1) / p.tiles);
-  if (p.splits < 1) p.splits = 1;
-  return p;
-}
-
 size_t pad16(size_t n) { return (n + 15) & ~(size_t)15; }
+
+// The workspace for `runs` runs; with ws null only its size.
+size_t make_work(int runs, int G, int64_t max_new, void* ws, Work* w) {
+  const int64_t rows = max_new * G < 256 ? max_new * G : 256;
+  const size_t head = 64, firsts = pad16(runs * sizeof(First)), states = pad16((size_t)2 * runs * rows * 4);
+  w->rows = (int)rows;
+  char* p = reinterpret_cast<char*>(ws);
+  w->cut = reinterpret_cast<Cut*>(p);
+  w->first = reinterpret_cast<First*>(p + head);
+  w->m = reinterpret_cast<float*>(p + head + firsts);
+  w->l = reinterpret_cast<float*>(p + head + firsts + states);
+  w->o = reinterpret_cast<float*>(p + head + firsts + 2 * states);
+  return head + firsts + 2 * states + (size_t)2 * runs * rows * 512;
+}
 
 }  // namespace
 
-size_t attn_paged_workspace(int num_seqs, int Hq, int Hkv, int64_t n_rows, int64_t max_new, int64_t max_t_quant,
-                            int max_t_res, int n_sink) {
-  const Plan p = make_plan(num_seqs, Hq, Hkv, n_rows, max_new, max_t_quant, max_t_res, n_sink);
-  if (p.splits == 1) return 16;
-  return 2 * pad16((size_t)p.splits * p.rows * 4) + (size_t)p.splits * p.rows * 512;
+size_t attn_paged_workspace(int G, int64_t max_new) {
+  Work w;
+  return make_work(device_sm_count(), G, max_new, nullptr, &w);
 }
 
 cudaError_t launch_attn_paged(const AttnArgs& a, cudaStream_t s) {
-  Plan p = make_plan(a.b.num_seqs, a.Hq, a.L.Hkv, a.b.n_rows, a.b.max_rows, a.max_t_quant, a.max_t_res, a.b.n_sink);
-  const size_t part = pad16((size_t)p.splits * p.rows * 4);
-  p.m = reinterpret_cast<float*>(a.ws);
-  p.l = reinterpret_cast<float*>(reinterpret_cast<char*>(a.ws) + part);
-  p.o = reinterpret_cast<float*>(reinterpret_cast<char*>(a.ws) + 2 * part);
-  const unsigned blocks = (unsigned)row_blocks(a.b.num_seqs, a.G, a.b.n_rows);
+  const int runs = device_sm_count();
+  Work w;
+  make_work(runs, a.G, a.b.max_rows, a.ws, &w);
   cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(attn_tc_kernel, dim3(blocks, a.L.Hkv, p.splits), dim3(kThreads), kSmem, s, a, p);
-  if (e != cudaSuccess || p.splits == 1) return e;
-  return launch_pdl(attn_merge_kernel, dim3(blocks, a.L.Hkv), dim3(256), 0, s, a, p);
+  e = launch_pdl(attn_tc_kernel, dim3(runs), dim3(kThreads), kSmem, s, a, w);
+  if (e != cudaSuccess || runs < 2) return e;
+  return launch_pdl(attn_merge_kernel, dim3(runs - 1, w.rows > 64 ? 4 : 1), dim3(256), 0, s, a, w);
 }
 
 }  // namespace kvq

@@ -210,8 +210,7 @@ struct AttnArgs {
   const void* res[2];
   int32_t* status;
 };
-size_t attn_paged_workspace(int num_seqs, int Hq, int Hkv, int64_t n_rows, int64_t max_new, int64_t max_t_quant,
-                            int max_t_res, int n_sink);
+size_t attn_paged_workspace(int G, int64_t max_new);
 cudaError_t launch_attn_paged(const AttnArgs& a, cudaStream_t s);
 
 // ---------------------------------------------------------------------------

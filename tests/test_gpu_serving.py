@@ -477,7 +477,10 @@ def test_attention_bounds_are_flagged_not_followed():
     kvq.attention_paged(p.fmt, p.gpu, ints(cu_of(counts)), 5, ints(p.tq), ints(p.tr), 256, max(p.tr), dev(q, BF16),
                         scale, out_dtype=F32, out=out, status=p.status)
     assert int(p.status) == kvq.KVQ_DEV_BOUNDS
-    assert torch.all(out[:3] == 3.0) and torch.equal(out[3:], clean[3:])
+    assert torch.all(out[:3] == 3.0)
+    # the others: with sequence 0 gone the work is cut at other tiles, so the sums round otherwise
+    # (not bit for bit the same), within the bars that hold for any cut
+    p.check_attention(q, scale, out, None, counts, True, F32, seqs=(1, 2))
     # rows behind the last sequence and rows of an empty one
     out = torch.full((20, 8, 128), 3.0, device="cuda")
     q2 = torch.cat([dev(q, BF16), dev(q, BF16)])[:20]
