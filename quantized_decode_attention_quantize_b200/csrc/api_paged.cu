@@ -43,6 +43,7 @@ bool paged_format(const kvq_format* f) {
 }
 
 constexpr int64_t kMaxRows = (int64_t)1 << 30;
+constexpr size_t kMaxTiles = (size_t)4 << 30;   // expanded pages that a workspace is sized for
 
 // Checks shared by the calls over a paged cache, and its device-side numbers.
 kvq_status paged_batch(const kvq_format* f, const kvq_paged_cache* pc, const int32_t* cu, int64_t n_rows,
@@ -224,7 +225,12 @@ static kvq_status attn_sizes(const kvq_format* f, int32_t num_seqs, int32_t Hq, 
 size_t kvq_attention_paged_workspace_bytes(const kvq_format* f, int32_t num_seqs, int32_t Hq, int32_t Hkv,
                                            int64_t n_rows, int64_t max_new, int64_t max_tq, int32_t max_tr) {
   if (attn_sizes(f, num_seqs, Hq, Hkv, n_rows, max_new, max_tq, max_tr) != KVQ_OK) return 0;
-  return attn_paged_workspace(Hq / Hkv, max_new);
+  size_t n = attn_paged_workspace(Hq / Hkv, max_new);
+  if (attn_wide_pays(num_seqs, Hq / Hkv, n_rows)) {
+    const size_t tiles = attn_wide_tiles(num_seqs, Hkv, max_tq, max_tr, f->n_sink);
+    if (tiles <= kMaxTiles) n += tiles;
+  }
+  return n;
 }
 
 kvq_status kvq_attention_paged(const kvq_format* f, const kvq_paged_cache* pc, const int32_t* cu, int64_t n_rows,
@@ -258,6 +264,7 @@ kvq_status kvq_attention_paged(const kvq_format* f, const kvq_paged_cache* pc, c
   a.out_dtype = out_dtype;
   a.lse = lse;
   a.ws = ws;
+  a.ws_bytes = ws_bytes;
   a.sink[0] = pc->sink_k;
   a.sink[1] = pc->sink_v;
   a.res[0] = pc->res_k;

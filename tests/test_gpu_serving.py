@@ -382,6 +382,26 @@ def test_attention_one_sequence(n, L, G):
     p.check_attention(q, scale, out, lse, [n], True, F32)
 
 
+@pytest.mark.parametrize("kw,causal", [(dict(), True), (dict(n_sink=200, k_rotate=1), True), (dict(src_dtype=F16), False)])
+def test_attention_long_chunks_with_and_without_expanded_pages(kw, causal):
+    # chunks of several row blocks: with the workspace asked for the pages are expanded first, with the
+    # smallest one they are not; block remainders of 1 .. 128 and of 129 .. 256 rows, windows that the
+    # first rows of a chunk do not see
+    p = Paged(fmt(**kw), 2, 3, 14, seed=49)
+    p.fill([900, 1500, 330])
+    counts = [257, 400, 330]
+    full = kvq.attention_paged_workspace_bytes(p.fmt, 3, 8, 2, sum(counts), max(counts), max(p.tq), max(p.tr))
+    least = kvq.attention_paged_workspace_bytes(p.fmt, 60000, 8, 2, sum(counts), max(counts), max(p.tq), max(p.tr))
+    assert full - least == 3 * 2 * 65536 * (-(-max(p.tq) // 128) + -(-(p.fd["n_sink"] + max(p.tr)) // 128))
+    q, scale, out, lse = p.attend(counts, 4, causal=causal)
+    assert int(p.status) == 0
+    p.check_attention(q, scale, out, lse, counts, causal, F32)
+    ws = torch.empty(least, dtype=torch.uint8, device="cuda")
+    _, _, out, lse = p.attend(counts, 4, causal=causal, q=q, workspace=ws)
+    assert int(p.status) == 0
+    p.check_attention(q, scale, out, lse, counts, causal, F32)
+
+
 def test_attention_many_short_sequences():
     p = Paged(fmt(), 1, 40, 2, seed=41)
     lengths = [int(x) for x in p.rng.integers(1, 200, 40)]
