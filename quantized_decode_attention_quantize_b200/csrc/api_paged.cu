@@ -216,8 +216,9 @@ static kvq_status attn_sizes(const kvq_format* f, int32_t num_seqs, int32_t Hq, 
   if (s != KVQ_OK) return s;
   if (num_seqs < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv) return KVQ_ERR_INVALID;
   if (n_rows < 0 || n_rows > kMaxRows || max_new < 0 || max_new > n_rows) return KVQ_ERR_INVALID;
-  if (max_tq < 0 || max_tr < 0 || max_tr > f->residual_cap || max_tq >= (int64_t)1 << 31) return KVQ_ERR_INVALID;
-  if (!paged_format(f) || Hq / Hkv > 16 || Hkv > 32767 || num_seqs > 65535 || n_rows * Hq >= (int64_t)1 << 31)
+  if (max_tq < 0 || max_tr < 0 || max_tr > f->residual_cap) return KVQ_ERR_INVALID;
+  if (!paged_format(f) || Hq / Hkv > 16 || Hkv > 32767 || num_seqs > 65535 || n_rows * Hq >= (int64_t)1 << 31 ||
+      max_tq >= (int64_t)1 << 30)
     return KVQ_ERR_UNSUPPORTED;
   return KVQ_OK;
 }

@@ -183,16 +183,15 @@ __device__ __forceinline__ void softmax_warp(const AttnArgs& a, const Work& work
     const int64_t out_row = (c.row0 + (c.r0 + r) / a.G) * a.Hq + c.h * a.G + (c.r0 + r) % a.G;
     if (c.N == 0) {   // no token for any row
       if (r < c.nr && !(c.split && w)) {
-        const float zero[8] = {};
-        for (int i = 0; i < 8; ++i) put8(a, work, c, out_row, r, 64 * hf + 8 * i, zero, 0.0f);
+        for (int i = 64 * hf; i < 64 * hf + 64; ++i) store_elem(a.out, out_row * 128 + i, a.out_dtype, 0.0f);
         if (a.lse && hf == 0) a.lse[out_row] = -INFINITY;
       }
       seg_done(sm, k, lane);
       continue;
     }
     bool bad = false;
-    if (!c.split) bad = stage_queries(a, c, sm, qs, w, warp & 7, 8, lane);
-    else bad = stage_queries(a, c, sm, qs, 0, warp, 16, lane);
+    if (!c.split) bad = stage_queries<8>(a, c, sm, qs, w, warp & 7, lane);
+    else bad = stage_queries<16>(a, c, sm, qs, 0, warp, lane);
     if (__any_sync(0xffffffffu, bad) && lane == 0) flag(a.status, KVQ_DEV_NONFINITE);
     fence_async_smem();
     tc_fence_before();
@@ -287,22 +286,19 @@ __device__ __forceinline__ void softmax_warp(const AttnArgs& a, const Work& work
       if (!sync2(&sm->row_pair[4 * w + (warp & 3)], &n_rows)) return;
       l += sm->mx[w][hf ^ 1][row];
     }
+    // boxes over Q: one per warp, or in a split block one per part of the warp's rows
+    uint8_t* box = smem + (c.split ? 2 * hf * 16384 : w * kTile + hf * 16384) + 4096 * (warp & 3);
+    const int box_step = c.split ? 16384 : 0;
+    uint32_t o[8][4];
     float f0 = 1.0f, f1 = 0.0f;
-    float4* other = reinterpret_cast<float4*>(smem) + (hf * 128 + row) * 16;   // 64 floats of this row, over Q
     if (two) {
       if (w == 1) {
         sm->m1[row] = m;
         sm->l1[row] = l;
 #pragma unroll 1
-        for (int e = 0; e < 8; ++e) {
-          uint32_t o[8];
-          tmem_ld8(o_col + 64 * hf + 8 * e, o);
-          tmem_wait_ld();
-          pin(o);
-          other[(2 * e) ^ (lane & 15)] = make_float4(__uint_as_float(o[0]), __uint_as_float(o[1]), __uint_as_float(o[2]),
-                                                     __uint_as_float(o[3]));
-          other[(2 * e + 1) ^ (lane & 15)] = make_float4(__uint_as_float(o[4]), __uint_as_float(o[5]),
-                                                         __uint_as_float(o[6]), __uint_as_float(o[7]));
+        for (int p = 0; p < 2; ++p) {
+          load_part(o_col, 2 * hf + p, o);
+          box_part(box + p * box_step, lane, o, 1.0f, false, 0.0f);
         }
       }
       if (!sync2(&sm->row_quad[warp & 3], &n_quads)) return;
@@ -314,8 +310,7 @@ __device__ __forceinline__ void softmax_warp(const AttnArgs& a, const Work& work
         m = mm;
       }
     }
-    if (w == 0 || !c.split) {
-      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    if (live && (w == 0 || !c.split)) {
       if (r < c.nr && hf == 0) {
         if (c.slot >= 0) {
           work.m[(int64_t)c.slot * work.rows + r] = m;
@@ -324,33 +319,14 @@ __device__ __forceinline__ void softmax_warp(const AttnArgs& a, const Work& work
           a.lse[out_row] = l > 0.0f ? kLn2 * (m + log2f(l) - kLift) : -INFINITY;
         }
       }
-      // columns 16 c + W hold channel 8 W + c: eight loads of four columns give four octets, W = 4 i ..; this
-      // half of the threads takes W = 8 hf .. 8 hf + 7
+      const float inv = c.slot >= 0 ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
+      int rows[8];
+      store_rows(a, work, c, r - lane, lane, rows);
 #pragma unroll 1
-      for (int i = 0; i < 2; ++i) {
-        uint32_t o[8][4];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) tmem_ld4(o_col + 16 * e + 8 * hf + 4 * i, o[e]);
-        tmem_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 8; ++e) pin(o[e]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float x[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(o[e][j]);
-          if (two) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {   // column 16 e + W of the other stream
-              const int col = 16 * e + 8 * hf + 4 * i + j;
-              const float* y = reinterpret_cast<const float*>(reinterpret_cast<float4*>(smem) +
-                                                              ((col >> 6) * 128 + row) * 16 +
-                                                              (((col & 63) >> 2) ^ (lane & 15)));
-              x[e] = x[e] * f0 + y[col & 3] * f1;
-            }
-          }
-          if (r < c.nr) put8(a, work, c, out_row, r, 8 * (8 * hf + 4 * i + j), x, inv);
-        }
+      for (int p = 0; p < 2; ++p) {   // this half's words of the rows
+        load_part(o_col, 2 * hf + p, o);
+        box_part(box + p * box_step, lane, o, f0 * inv, two, f1 * inv);
+        store_part(a, work, c, box + p * box_step, rows, 2 * hf + p, lane);
       }
     }
     tc_fence_before();
@@ -473,7 +449,7 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const __grid_constant__
 namespace attn {
 cudaError_t launch_merge(const AttnArgs& a, const Work& w, int runs, cudaStream_t s) {
   if (runs < 2) return cudaSuccess;
-  return launch_pdl(attn_merge_kernel, dim3(runs - 1, w.rows > 64 ? 4 : 1), dim3(256), 0, s, a, w);
+  return launch_pdl(attn_merge_kernel, dim3(runs - 1, (w.rows + 7) / 8), dim3(256), 0, s, a, w);
 }
 }  // namespace attn
 

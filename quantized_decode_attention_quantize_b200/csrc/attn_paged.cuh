@@ -57,29 +57,27 @@ struct Seen {
   int raw, packed;
 };
 __device__ __forceinline__ Seen row_seen(const AttnArgs& a, const AttnSeq& q, int i) {
-  const int ns = a.b.n_sink;
-  const int64_t L = (int64_t)ns + q.tq + q.tr;
-  const int64_t see = a.causal ? max((int64_t)0, min(L, L - q.n + i + 1)) : L;
-  const int64_t behind = see - ns;        // of packed and window tokens
+  const int ns = a.b.n_sink, L = ns + q.tq + q.tr;   // the host keeps all of these below 2^31
+  const int see = a.causal ? max(0, min(L, L - q.n + i + 1)) : L;
+  const int behind = see - ns;            // of packed and window tokens
   Seen r;
-  r.packed = (int)min(max(behind, (int64_t)0), (int64_t)q.tq);
-  r.raw = (int)min(see, (int64_t)ns) + (int)max(behind - q.tq, (int64_t)0);
+  r.packed = min(max(behind, 0), q.tq);
+  r.raw = min(see, ns) + max(behind - q.tq, 0);
   return r;
 }
 
 // Row blocks of a sequence and the KV tiles the last row of block b sees.
 __device__ __forceinline__ int seq_blocks(const AttnArgs& a, const AttnSeq& q) {
-  return (int)(((int64_t)q.n * a.G + 255) / 256);
+  return (q.n * a.G + 255) >> 8;
 }
 __device__ __forceinline__ int block_tiles(const AttnArgs& a, const AttnSeq& q, int b) {
-  const int64_t last = min((int64_t)q.n * a.G, (int64_t)(b + 1) * 256) - 1;
-  const Seen v = row_seen(a, q, (int)(last / a.G));
-  return (v.raw + 127) / 128 + (v.packed + 127) / 128;
+  const Seen v = row_seen(a, q, (min(q.n * a.G, (b + 1) * 256) - 1) / a.G);
+  return ((v.raw + 127) >> 7) + ((v.packed + 127) >> 7);
 }
 
 // ---- the partition (one warp) ----------------------------------------------------------------
 // Units of a sequence's blocks (per KV head): tiles + 1 each.  `q` differs from lane to lane.
-__device__ __forceinline__ int64_t seq_units(const AttnArgs& a, const AttnSeq& q, int lane) {
+static __device__ __noinline__ int64_t seq_units(const AttnArgs& a, const AttnSeq& q, int lane) {
   const int nb = q.ok ? seq_blocks(a, q) : 0;
   int64_t w = nb == 1 ? block_tiles(a, q, 0) + 1 : 0;
   unsigned many = __ballot_sync(0xffffffffu, nb > 1);
@@ -108,14 +106,12 @@ __device__ __forceinline__ int64_t scan64(int64_t v, int lane) {   // inclusive
   return v;
 }
 
-// All units, and the number of runs they are cut into.
+// All units, and the number of runs they are cut into: the first `longer` of them one unit longer than `each`.
 struct Cut {
-  int64_t units;
-  int runs;
+  int64_t units, each;
+  int runs, longer;
 };
-__host__ __device__ __forceinline__ int64_t run_start(const Cut& c, int i) {
-  return (int64_t)((__int128)c.units * i / c.runs);
-}
+__device__ __forceinline__ int64_t run_start(const Cut& c, int i) { return c.each * i + min(i, c.longer); }
 __device__ __forceinline__ Cut find_cut(const AttnArgs& a, int lane) {
   int64_t total = 0;
   bool bad = false;
@@ -131,6 +127,8 @@ __device__ __forceinline__ Cut find_cut(const AttnArgs& a, int lane) {
   Cut c;
   c.units = total * a.L.Hkv;
   c.runs = (int)max((int64_t)1, min((int64_t)gridDim.x, c.units / kMinRun));
+  c.each = c.units / c.runs;
+  c.longer = (int)(c.units - c.each * c.runs);
   return c;
 }
 
@@ -183,9 +181,9 @@ __device__ __forceinline__ Place find_place(const AttnArgs& a, int64_t at, int l
       const int l = hit ? __ffs(hit) - 1 : b0;
       at -= __shfl_sync(0xffffffffu, incl - w, l);
       p.b = b0 - l;
-      const int64_t one = __shfl_sync(0xffffffffu, w, l) / a.L.Hkv;
+      const int one = block_tiles(a, p.q, p.b) + 1;
       p.h = (int)(at / one);
-      *unit = at % one;
+      *unit = at - (int64_t)p.h * one;
       return p;
     }
     at -= __shfl_sync(0xffffffffu, incl, 31);
@@ -399,7 +397,7 @@ __device__ __forceinline__ void announce(const AttnArgs& a, const Work& work, Sm
       c.tq = p.q.tq;
       c.tr = p.q.tr;
       c.r0 = p.b * 256;
-      c.nr = (int)min((int64_t)256, (int64_t)p.q.n * a.G - c.r0);
+      c.nr = min(256, p.q.n * a.G - c.r0);
       c.split = c.nr <= 128;
       const Seen last = row_seen(a, p.q, (c.r0 + c.nr - 1) / a.G);
       c.raw = last.raw;
@@ -592,99 +590,160 @@ __device__ __forceinline__ void chunk_weights(const uint32_t (&x)[32], uint64_t 
   }
 }
 
-// The queries of 128 rows (tile w) by `warps` warps: a warp per row, four channels per lane, four
-// rows at a time; scaled so that the row's largest lies in [2^8, 2^9).
-template <typename Small>
+// The queries of 128 rows (tile w) by WARPS warps: a warp per row, four channels per lane; scaled so that
+// the row's largest lies in [2^8, 2^9).  16-bit rows are first copied, all of them in flight, to where the
+// tile holds them (two segments of 128 bytes each), then turned in place; fp32 rows are read one by one.
+// Loops stay short: this code runs once per block, and would otherwise wait for its instructions.
+template <int WARPS, typename Small>
 __device__ __forceinline__ bool stage_queries(const AttnArgs& a, const Seg& c, Small* sm, uint32_t qs, int w, int wi,
-                                              int warps, int lane) {
+                                              int lane) {
   bool bad = false;
-#pragma unroll 1
-  for (int rb = 128 * w + wi; rb < 128 * w + 128; rb += 4 * warps) {
-    uint4 v[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int r = rb + k * warps;
-      v[k] = make_uint4(0, 0, 0, 0);
+  const int r0 = 128 * w + wi;
+  const int t0 = (c.r0 + r0) / a.G, g0 = c.r0 + r0 - t0 * a.G, ts = WARPS / a.G, gs = WARPS - ts * a.G;
+  const uint32_t tile = qs + w * kTile + (lane >> 4) * 16384;
+  const int64_t head = c.row0 * a.Hq + c.h * a.G;
+  auto advance = [&](int& t, int& g) {   // WARPS rows on
+    t += ts;
+    g += gs;
+    if (g >= a.G) {
+      g -= a.G;
+      ++t;
+    }
+  };
+  const bool wide = a.q_dtype == KVQ_F32;
+  if (!wide) {
+    int t = t0, g = g0;
+#pragma unroll 2
+    for (int r = r0; r < 128 * w + 128; r += WARPS) {
+      const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + (head + (int64_t)t * a.Hq + g) * 128 + 4 * lane;
+      const uint32_t dst = tile + (r & 127) * 128 + (lane & 15) * 8;
+      if (r < c.nr) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+      else asm volatile("st.shared.v2.b32 [%0], {%1, %1};" ::"r"(dst), "r"(0) : "memory");
+      advance(t, g);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+  }
+  int t = t0, g = g0;
+#pragma unroll 4
+  for (int r = r0; r < 128 * w + 128; r += WARPS) {
+    float x[4] = {0, 0, 0, 0};
+    const uint32_t row = tile + (r & 127) * 128;
+    if (wide) {
       if (r < c.nr) {
-        const int64_t e = ((c.row0 + (c.r0 + r) / a.G) * a.Hq + c.h * a.G + (c.r0 + r) % a.G) * 128 + 4 * lane;
-        if (a.q_dtype == KVQ_F32) {
-          v[k] = *reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(a.q) + e);
-        } else {
-          const uint2 u = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(a.q) + e);
-          v[k].x = u.x;
-          v[k].y = u.y;
-        }
+        const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.q) +
+                                                          (head + (int64_t)t * a.Hq + g) * 128 + 4 * lane);
+        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
       }
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int r = rb + k * warps;
-      float x[4];
-      if (a.q_dtype == KVQ_F32) {
-        x[0] = __uint_as_float(v[k].x); x[1] = __uint_as_float(v[k].y);
-        x[2] = __uint_as_float(v[k].z); x[3] = __uint_as_float(v[k].w);
-      } else if (a.q_dtype == KVQ_F16) {
-        x[0] = half_bits_to_float((uint16_t)(v[k].x & 0xffffu)); x[1] = half_bits_to_float((uint16_t)(v[k].x >> 16));
-        x[2] = half_bits_to_float((uint16_t)(v[k].y & 0xffffu)); x[3] = half_bits_to_float((uint16_t)(v[k].y >> 16));
+      advance(t, g);
+    } else {
+      uint32_t u, v;
+      asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(u), "=r"(v) : "r"(row + (lane & 15) * 8) : "memory");
+      if (a.q_dtype == KVQ_F16) {
+        x[0] = half_bits_to_float((uint16_t)(u & 0xffffu)); x[1] = half_bits_to_float((uint16_t)(u >> 16));
+        x[2] = half_bits_to_float((uint16_t)(v & 0xffffu)); x[3] = half_bits_to_float((uint16_t)(v >> 16));
       } else {
-        x[0] = __uint_as_float(v[k].x << 16); x[1] = __uint_as_float(v[k].x & 0xffff0000u);
-        x[2] = __uint_as_float(v[k].y << 16); x[3] = __uint_as_float(v[k].y & 0xffff0000u);
+        x[0] = __uint_as_float(u << 16); x[1] = __uint_as_float(u & 0xffff0000u);
+        x[2] = __uint_as_float(v << 16); x[3] = __uint_as_float(v & 0xffff0000u);
       }
-      bad |= !(isfinite(x[0]) && isfinite(x[1]) && isfinite(x[2]) && isfinite(x[3]));
-      if (a.L.k_rotate) {
-        wht128_quad_unscaled(x, lane);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] *= a.L.rot_scale;
-      }
-      const float top = warp_max(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
-      // 2^(e - 127) <= top < 2^(e - 126); zero, subnormal or overflowing rows get the nearest e that serves
-      const int e = min(max((int)(__float_as_uint(top) >> 23), 10), 250);
-      const float up = __uint_as_float((uint32_t)(262 - e) << 23);   // 2^(8 - (e - 127))
-      if (lane == 0) sm->rowscale[r] = __uint_as_float((uint32_t)(e - 8) << 23);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] *= up;
-      const bool odd = lane & 1;
-      const float y0 = __shfl_xor_sync(0xffffffffu, odd ? x[0] : x[2], 1);
-      const float y1 = __shfl_xor_sync(0xffffffffu, odd ? x[1] : x[3], 1);
-      const uint32_t h0 = odd ? pack_f16(y0, x[2]) : pack_f16(x[0], y0);
-      const uint32_t h1 = odd ? pack_f16(y1, x[3]) : pack_f16(x[1], y1);
-      const int o = lane >> 1;
-      const uint32_t at = qs + w * kTile + (o >> 3) * 16384 + (r & 127) * 128 + (((o & 7) ^ (r & 7)) << 4) + 8 * odd;
-      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(h0), "r"(h1) : "memory");
     }
+    // the largest magnitude, as the bits of a positive number; those of Inf and NaN are the largest
+    auto magnitude = [](float y) { return __float_as_uint(y) & 0x7fffffffu; };
+    if (a.L.k_rotate) {
+      bad |= max(max(magnitude(x[0]), magnitude(x[1])), max(magnitude(x[2]), magnitude(x[3]))) >= 0x7f800000u;
+      wht128_quad_unscaled(x, lane);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] *= a.L.rot_scale;
+    }
+    const uint32_t top = __reduce_max_sync(0xffffffffu, max(max(magnitude(x[0]), magnitude(x[1])),
+                                                            max(magnitude(x[2]), magnitude(x[3]))));
+    bad |= top >= 0x7f800000u;
+    // 2^(e - 127) <= top < 2^(e - 126); zero, subnormal or overflowing rows get the nearest e that serves
+    const int e = min(max((int)(top >> 23), 10), 250);
+    const float up = __uint_as_float((uint32_t)(262 - e) << 23);   // 2^(8 - (e - 127))
+    if (lane == 0) sm->rowscale[r] = __uint_as_float((uint32_t)(e - 8) << 23);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] *= up;
+    const bool odd = lane & 1;
+    const float y0 = __shfl_xor_sync(0xffffffffu, odd ? x[0] : x[2], 1);
+    const float y1 = __shfl_xor_sync(0xffffffffu, odd ? x[1] : x[3], 1);
+    const uint32_t h0 = odd ? pack_f16(y0, x[2]) : pack_f16(x[0], y0);
+    const uint32_t h1 = odd ? pack_f16(y1, x[3]) : pack_f16(x[1], y1);
+    // every lane has read its part of the row (the reduction above)
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(row + ((((lane >> 1) & 7) ^ (r & 7)) << 4) + 8 * odd), "r"(h0),
+                 "r"(h1)
+                 : "memory");
   }
   return bad;
 }
 
-// Eight channels of a row, to the output or to a partial slot.
-__device__ __forceinline__ void put8(const AttnArgs& a, const Work& work, const Seg& c, int64_t row, int r, int ch,
-                                     const float (&x)[8], float inv) {
-  if (c.slot >= 0) {
-    float4* d = reinterpret_cast<float4*>(work.o + ((int64_t)c.slot * work.rows + r) * 128 + ch);
-    d[0] = make_float4(x[0], x[1], x[2], x[3]);
-    d[1] = make_float4(x[4], x[5], x[6], x[7]);
-    return;
-  }
-  if (a.out_dtype == KVQ_F32) {
-    float4* d = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + row * 128 + ch);
-    d[0] = make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-    d[1] = make_float4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv);
-    return;
-  }
-  uint32_t h[4];
+// ---- the way out ------------------------------------------------------------------------------------
+// A warp's 32 rows go out 32 channels at a time (words W = 4 part .. + 3) through 4 KB of shared memory, rows
+// of 128 bytes with 16-byte chunk c of row i at c ^ (i % 8): a thread writes its row's chunks, then eight
+// lanes each read and store a row's.  Columns 16 c + W of O hold channel 8 W + c.
+__device__ __forceinline__ float4* out_chunk(uint8_t* box, int i, int c) {
+  return reinterpret_cast<float4*>(box + 128 * i + 16 * (c ^ (i & 7)));
+}
+// This thread's 32 channels of part `part`: o[e][j] is channel 8 (4 part + j) + e.
+__device__ __forceinline__ void load_part(uint32_t o_col, int part, uint32_t (&o)[8][4]) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float u = x[2 * e] * inv, v = x[2 * e + 1] * inv;
-    if (a.out_dtype == KVQ_F16) {
-      h[e] = pack_f16(u, v);
+  for (int e = 0; e < 8; ++e) tmem_ld4(o_col + 16 * e + 4 * part, o[e]);
+  tmem_wait_ld();
+#pragma unroll
+  for (int e = 0; e < 8; ++e) pin(o[e]);
+}
+// f * o (+ g * what the box holds) into the box, as channels in order: chunk 2 j + (e / 4).
+__device__ __forceinline__ void box_part(uint8_t* box, int lane, const uint32_t (&o)[8][4], float f, bool add, float g) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float4* at = out_chunk(box, lane, 2 * j + k);
+      float4 v = make_float4(__uint_as_float(o[4 * k][j]) * f, __uint_as_float(o[4 * k + 1][j]) * f,
+                             __uint_as_float(o[4 * k + 2][j]) * f, __uint_as_float(o[4 * k + 3][j]) * f);
+      if (add) {
+        const float4 u = *at;
+        v = make_float4(v.x + u.x * g, v.y + u.y * g, v.z + u.z * g, v.w + u.w * g);
+      }
+      *at = v;
+    }
+}
+// The rows that this lane stores: row i = 4 k + lane / 8 of the warp's, as a row of the output or of the
+// partial slot (the host keeps output rows below 2^31); -1 past the block's end.
+__device__ __forceinline__ void store_rows(const AttnArgs& a, const Work& work, const Seg& c, int first, int lane,
+                                           int (&rows)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int r = first + 4 * k + (lane >> 3), t = (c.r0 + r) / a.G;
+    rows[k] = r >= c.nr ? -1 : c.slot >= 0 ? c.slot * work.rows + r
+                                           : ((int)c.row0 + t) * a.Hq + c.h * a.G + (c.r0 + r - t * a.G);
+  }
+}
+__device__ __forceinline__ void store_part(const AttnArgs& a, const Work& work, const Seg& c, uint8_t* box,
+                                           const int (&rows)[8], int part, int lane) {
+  __syncwarp();
+  const bool wide = c.slot >= 0 || a.out_dtype == KVQ_F32;
+  void* to = c.slot >= 0 ? work.o : a.out;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float4 v = *out_chunk(box, 4 * k + (lane >> 3), lane & 7);
+    if (rows[k] < 0) continue;
+    const int64_t at = (int64_t)rows[k] * 128 + 32 * part + 4 * (lane & 7);
+    if (wide) {
+      *reinterpret_cast<float4*>(reinterpret_cast<float*>(to) + at) = v;
     } else {
-      const __nv_bfloat162 b2 = __floats2bfloat162_rn(u, v);
-      h[e] = *reinterpret_cast<const uint32_t*>(&b2);
+      uint2 h;
+      if (a.out_dtype == KVQ_F16) {
+        h = make_uint2(pack_f16(v.x, v.y), pack_f16(v.z, v.w));
+      } else {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(v.x, v.y), q = __floats2bfloat162_rn(v.z, v.w);
+        h = make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
+      }
+      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(to) + at) = h;
     }
   }
-  *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + row * 128 + ch) = make_uint4(h[0], h[1], h[2], h[3]);
+  __syncwarp();
 }
-
 inline size_t pad16(size_t n) { return (n + 15) & ~(size_t)15; }
 // The workspace for `runs` runs; with ws null only its size.
 inline size_t make_work(int runs, int G, int64_t max_new, void* ws, Work* w) {

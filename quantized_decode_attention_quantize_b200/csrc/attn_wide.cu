@@ -181,15 +181,14 @@ __device__ __forceinline__ void softmax_warp(const AttnArgs& a, const Work& work
     const int64_t out_row = (c.row0 + (c.r0 + r) / a.G) * a.Hq + c.h * a.G + (c.r0 + r) % a.G;
     if (c.N == 0) {   // no token for any row
       if (r < c.nr && !(c.split && w)) {
-        const float zero[8] = {};
-        for (int i = 0; i < 16; ++i) put8(a, work, c, out_row, r, 8 * i, zero, 0.0f);
+        for (int i = 0; i < 128; ++i) store_elem(a.out, out_row * 128 + i, a.out_dtype, 0.0f);
         if (a.lse) a.lse[out_row] = -INFINITY;
       }
       seg_done(sm, k, lane);
       continue;
     }
-    const bool bad = c.split ? stage_queries(a, c, sm, qs, 0, warp, 8, lane)
-                             : stage_queries(a, c, sm, qs, w, warp & 3, 4, lane);
+    const bool bad = c.split ? stage_queries<8>(a, c, sm, qs, 0, warp, lane)
+                             : stage_queries<4>(a, c, sm, qs, w, warp & 3, lane);
     if (__any_sync(0xffffffffu, bad) && lane == 0) flag(a.status, KVQ_DEV_NONFINITE);
     fence_async_smem();
     tc_fence_before();
@@ -277,22 +276,19 @@ __device__ __forceinline__ void softmax_warp(const AttnArgs& a, const Work& work
     if (two && w == 1 && !mbar_wait(smem_u32(&sm->o_full[0]), blocks & 1, stop)) return;
     ++blocks;
     tc_fence_after();
+    // boxes over Q: one per warp, or in a split block one per part of the warp's rows
+    uint8_t* box = smem + (c.split ? 0 : w * kTile) + 4096 * (warp & 3);
+    const int box_step = c.split ? 16384 : 0;
+    uint32_t o[8][4];
     float f0 = 1.0f, f1 = 0.0f;
-    float4* other = reinterpret_cast<float4*>(smem) + row * 32;   // 128 floats of this row, over Q
     if (two) {
       if (w == 1) {
         sm->m1[row] = m;
         sm->l1[row] = l;
 #pragma unroll 1
-        for (int e = 0; e < 16; ++e) {
-          uint32_t o[8];
-          tmem_ld8(o_col + 8 * e, o);
-          tmem_wait_ld();
-          pin(o);
-          other[(2 * e) ^ lane] = make_float4(__uint_as_float(o[0]), __uint_as_float(o[1]), __uint_as_float(o[2]),
-                                              __uint_as_float(o[3]));
-          other[(2 * e + 1) ^ lane] = make_float4(__uint_as_float(o[4]), __uint_as_float(o[5]), __uint_as_float(o[6]),
-                                                  __uint_as_float(o[7]));
+        for (int p = 0; p < 4; ++p) {
+          load_part(o_col, p, o);
+          box_part(box + p * box_step, lane, o, 1.0f, false, 0.0f);
         }
       }
       if (!sync(&sm->row_pair[warp & 3], &n_pair)) return;
@@ -304,8 +300,7 @@ __device__ __forceinline__ void softmax_warp(const AttnArgs& a, const Work& work
         m = mm;
       }
     }
-    if (w == 0 || !c.split) {
-      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    if (live && (w == 0 || !c.split)) {
       if (r < c.nr) {
         if (c.slot >= 0) {
           work.m[(int64_t)c.slot * work.rows + r] = m;
@@ -314,29 +309,14 @@ __device__ __forceinline__ void softmax_warp(const AttnArgs& a, const Work& work
           a.lse[out_row] = l > 0.0f ? kLn2 * (m + log2f(l) - kLift) : -INFINITY;
         }
       }
-      // columns 16 c + W hold channel 8 W + c: eight loads of four columns give four octets
+      const float inv = c.slot >= 0 ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
+      int rows[8];
+      store_rows(a, work, c, r - lane, lane, rows);
 #pragma unroll 1
-      for (int i = 0; i < 4; ++i) {
-        uint32_t o[8][4];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) tmem_ld4(o_col + 16 * e + 4 * i, o[e]);
-        tmem_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 8; ++e) pin(o[e]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float x[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(o[e][j]);
-          if (two) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {   // column 16 e + 4 i + j of the other stream
-              const float* y = reinterpret_cast<const float*>(other + ((4 * e + i) ^ lane));
-              x[e] = x[e] * f0 + y[j] * f1;
-            }
-          }
-          if (r < c.nr) put8(a, work, c, out_row, r, 8 * (4 * i + j), x, inv);
-        }
+      for (int p = 0; p < 4; ++p) {
+        load_part(o_col, p, o);
+        box_part(box + p * box_step, lane, o, f0 * inv, two, f1 * inv);
+        store_part(a, work, c, box + p * box_step, rows, p, lane);
       }
     }
     tc_fence_before();
