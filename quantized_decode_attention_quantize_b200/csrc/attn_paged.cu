@@ -125,6 +125,16 @@ __device__ __forceinline__ void loader(const AttnArgs& a, const Work& work, Smal
           flags |= KVQ_DEV_BOUNDS;
           page = 0;
         }
+        if (g + lane < g1) {   // towards L2 now: the two stages alone would wait for memory
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            const Side& S = a.L.side[v];
+            const int64_t slab = (int64_t)page * a.L.Hkv + c.h;
+            prefetch_l2(reinterpret_cast<const uint8_t*>(S.codes) + slab * S.code_slab_bytes, v ? 4096 : 8192);
+            prefetch_l2(reinterpret_cast<const __half*>(S.scale) + slab * 128, 256);
+            prefetch_l2(reinterpret_cast<const __half*>(S.zero) + slab * 128, 256);
+          }
+        }
       }
       const int64_t slab = (int64_t)__shfl_sync(0xffffffffu, page, (g - g0) & 31) * a.L.Hkv + c.h;
       const int st = groups % kStages, use = groups / kStages;
@@ -458,15 +468,30 @@ cudaError_t launch_merge(const AttnArgs& a, const Work& w, int runs, cudaStream_
 // attn_wide_kernel).
 bool attn_wide_pays(int num_seqs, int G, int64_t n_rows) { return n_rows * G >= (int64_t)num_seqs * 512; }
 
-size_t attn_paged_workspace(int G, int64_t max_new) {
-  Work w;
-  return make_work(device_sm_count(), G, max_new, nullptr, &w);
+// Blocks of 16 rows, a warp each, up to 64 rows a sequence; blocks of 256 on the whole CTA above.
+constexpr int kNarrowRows = 64, kNarrowWarps = 8;
+bool narrow(int G, int64_t max_new) { return max_new * G <= kNarrowRows; }
+size_t make_work_for(int G, int64_t max_new, void* ws, Work* w, int* runs) {
+  *runs = device_sm_count() * (narrow(G, max_new) ? kNarrowWarps : 1);
+  return make_work(*runs, narrow(G, max_new) ? 16 : 256, G, max_new, ws, w);
 }
 
-cudaError_t launch_attn_paged(const AttnArgs& a, cudaStream_t s) {
-  const int runs = device_sm_count();
+size_t attn_paged_workspace(int G, int64_t max_new) {
   Work w;
-  const size_t small = make_work(runs, a.G, a.b.max_rows, a.ws, &w);
+  int runs;
+  return make_work_for(G, max_new, nullptr, &w, &runs);
+}
+
+cudaError_t launch_attn_paged(const AttnArgs& args, cudaStream_t s) {
+  AttnArgs a = args;
+  int runs;
+  Work w;
+  const size_t small = make_work_for(a.G, a.b.max_rows, a.ws, &w, &runs);
+  a.block = narrow(a.G, a.b.max_rows) ? 16 : 256;
+  if (a.block == 16) {
+    const cudaError_t e = launch_attn_narrow(a, w, runs, s);
+    return e != cudaSuccess ? e : launch_merge(a, w, runs, s);
+  }
   if (attn_wide_pays(a.b.num_seqs, a.G, a.b.n_rows) && a.ws_bytes >= small + attn_wide_bytes(a))
     return launch_attn_wide(a, w, runs, reinterpret_cast<char*>(a.ws) + small, s);
   cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);

@@ -17,7 +17,7 @@ constexpr int kStagesAt = kSlotsAt + kSlots * kTile;
 constexpr int kSegs = 2;                  // announced blocks
 constexpr float kLazy = 8.0f;             // log2 slack of the running maximum
 constexpr float kLift = 7.0f;             // log2 factor carried by the weights
-constexpr int kMinRun = 4;                // units of a run at least
+constexpr int kMinRun = 2;                // units of a run at least
 
 // The part of a block that this CTA does.
 struct Seg {
@@ -68,10 +68,10 @@ __device__ __forceinline__ Seen row_seen(const AttnArgs& a, const AttnSeq& q, in
 
 // Row blocks of a sequence and the KV tiles the last row of block b sees.
 __device__ __forceinline__ int seq_blocks(const AttnArgs& a, const AttnSeq& q) {
-  return (q.n * a.G + 255) >> 8;
+  return (q.n * a.G + a.block - 1) / a.block;
 }
 __device__ __forceinline__ int block_tiles(const AttnArgs& a, const AttnSeq& q, int b) {
-  const Seen v = row_seen(a, q, (min(q.n * a.G, (b + 1) * 256) - 1) / a.G);
+  const Seen v = row_seen(a, q, (min(q.n * a.G, (b + 1) * a.block) - 1) / a.G);
   return ((v.raw + 127) >> 7) + ((v.packed + 127) >> 7);
 }
 
@@ -112,7 +112,8 @@ struct Cut {
   int runs, longer;
 };
 __device__ __forceinline__ int64_t run_start(const Cut& c, int i) { return c.each * i + min(i, c.longer); }
-__device__ __forceinline__ Cut find_cut(const AttnArgs& a, int lane) {
+// q0, w0: the lane's sequence and its units among the first 32 (all, most often), for find_place.
+__device__ __forceinline__ Cut find_cut(const AttnArgs& a, int runs, int lane, AttnSeq* q0, int64_t* w0) {
   int64_t total = 0;
   bool bad = false;
   for (int s0 = 0; s0 < a.b.num_seqs; s0 += 32) {
@@ -121,12 +122,17 @@ __device__ __forceinline__ Cut find_cut(const AttnArgs& a, int lane) {
       q = attn_seq(a, s0 + lane);
       bad |= !q.ok;
     }
-    total += __shfl_sync(0xffffffffu, scan64(seq_units(a, q, lane), lane), 31);
+    const int64_t w = seq_units(a, q, lane);
+    if (s0 == 0) {
+      *q0 = q;
+      *w0 = w;
+    }
+    total += __shfl_sync(0xffffffffu, scan64(w, lane), 31);
   }
   if (blockIdx.x == 0 && __any_sync(0xffffffffu, bad) && lane == 0) flag(a.status, KVQ_DEV_BOUNDS);
   Cut c;
   c.units = total * a.L.Hkv;
-  c.runs = (int)max((int64_t)1, min((int64_t)gridDim.x, c.units / kMinRun));
+  c.runs = (int)max((int64_t)1, min((int64_t)runs, c.units / kMinRun));
   c.each = c.units / c.runs;
   c.longer = (int)(c.units - c.each * c.runs);
   return c;
@@ -156,22 +162,33 @@ __device__ __forceinline__ bool next_block(const AttnArgs& a, Place* p) {
   return next_seq(a, p);
 }
 // The block that holds unit `at`, and the unit's index in it.
-__device__ __forceinline__ Place find_place(const AttnArgs& a, int64_t at, int lane, int64_t* unit) {
+__device__ __forceinline__ Place find_place(const AttnArgs& a, int64_t at, int lane, const AttnSeq& q0, int64_t w0,
+                                            int64_t* unit) {
   Place p = {};
   for (int s0 = 0; s0 < a.b.num_seqs; s0 += 32) {
-    AttnSeq q = {};
-    if (s0 + lane < a.b.num_seqs) q = attn_seq(a, s0 + lane);
-    const int64_t w = seq_units(a, q, lane) * a.L.Hkv, incl = scan64(w, lane);
+    AttnSeq q = q0;
+    int64_t w = w0;
+    if (s0 > 0) {
+      q = {};
+      if (s0 + lane < a.b.num_seqs) q = attn_seq(a, s0 + lane);
+      w = seq_units(a, q, lane);
+    }
+    w *= a.L.Hkv;
+    const int64_t incl = scan64(w, lane);
     const unsigned hit = __ballot_sync(0xffffffffu, at < incl);
     if (hit) {
       const int l = __ffs(hit) - 1;
       at -= __shfl_sync(0xffffffffu, incl - w, l);
       p.s = s0 + l;
+      p.q.row0 = __shfl_sync(0xffffffffu, q.row0, l);
+      p.q.n = __shfl_sync(0xffffffffu, q.n, l);
+      p.q.tq = __shfl_sync(0xffffffffu, q.tq, l);
+      p.q.tr = __shfl_sync(0xffffffffu, q.tr, l);
+      p.q.ok = true;
       break;
     }
     at -= __shfl_sync(0xffffffffu, incl, 31);
   }
-  p.q = attn_seq(a, p.s);
   const int nb = seq_blocks(a, p.q);
   for (int b0 = nb - 1;; b0 -= 32) {   // lanes take blocks b0, b0 - 1, ...
     const int64_t w = b0 - lane >= 0 ? (int64_t)(block_tiles(a, p.q, b0 - lane) + 1) * a.L.Hkv : 0;
@@ -200,6 +217,7 @@ struct First {
 struct Work {
   Cut* cut;
   First* first;
+  int runs;              // at most
   int rows;              // of a slot
   float* m;              // [slots][rows]
   float* l;
@@ -371,53 +389,67 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                "l"(src), "r"(bytes), "r"(bar)
                : "memory");
 }
+__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+// What run `run` does of the block at p, from its unit `unit` on with `left` units to go; the run's first block
+// is noted for the merge.
+__device__ __forceinline__ Seg take_block(const AttnArgs& a, const Work& work, const Place& p, int tiles, int run,
+                                          int64_t unit, int64_t left, bool head, int lane) {
+  Seg c;
+  c.row0 = p.q.row0;
+  c.s = p.s;
+  c.h = p.h;
+  c.n = p.q.n;
+  c.tq = p.q.tq;
+  c.tr = p.q.tr;
+  c.r0 = p.b * a.block;
+  c.nr = min(a.block, p.q.n * a.G - c.r0);
+  c.split = c.nr <= 128;
+  const Seen last = row_seen(a, p.q, (c.r0 + c.nr - 1) / a.G);
+  c.raw = last.raw;
+  c.packed = last.packed;
+  c.n_raw = (c.raw + 127) / 128;
+  const int64_t end = min((int64_t)tiles + 1, unit + left);
+  c.t_lo = (int)max(unit - 1, (int64_t)0);
+  c.N = (int)max(end - 1 - c.t_lo, (int64_t)0);
+  c.slot = unit <= 1 && end == tiles + 1 ? -1 : 2 * run + (unit <= 1);
+  if (head && lane == 0) {
+    First f;
+    f.row0 = c.row0;
+    f.h = c.h;
+    f.r0 = c.r0;
+    f.nr = c.nr;
+    f.pad = 0;
+    f.unit = unit;
+    f.units = tiles + 1;
+    work.first[run] = f;
+  }
+  return c;
 }
 
 // One warp: finds this CTA's run, announces its blocks one by one and calls loads(block) after each (false:
 // stop); a last block with N < 0 ends the list.
 template <typename Small, typename Loads>
 __device__ __forceinline__ void announce(const AttnArgs& a, const Work& work, Small* sm, int lane, Loads loads) {
-  const Cut cut = find_cut(a, lane);
+  AttnSeq q0 = {};
+  int64_t w0 = 0;
+  const Cut cut = find_cut(a, work.runs, lane, &q0, &w0);
   const int run = blockIdx.x;
   if (run == 0 && lane == 0) *work.cut = cut;
   int k = 0;
   bool ok = true;
   if (run < cut.runs && cut.units > 0) {
     int64_t unit, left = run_start(cut, run + 1) - run_start(cut, run);
-    Place p = find_place(a, run_start(cut, run), lane, &unit);
+    Place p = find_place(a, run_start(cut, run), lane, q0, w0, &unit);
     for (bool head = true; left > 0 && ok; head = false) {
       const int tiles = block_tiles(a, p.q, p.b);
-      Seg c;
-      c.row0 = p.q.row0;
-      c.s = p.s;
-      c.h = p.h;
-      c.n = p.q.n;
-      c.tq = p.q.tq;
-      c.tr = p.q.tr;
-      c.r0 = p.b * 256;
-      c.nr = min(256, p.q.n * a.G - c.r0);
-      c.split = c.nr <= 128;
-      const Seen last = row_seen(a, p.q, (c.r0 + c.nr - 1) / a.G);
-      c.raw = last.raw;
-      c.packed = last.packed;
-      c.n_raw = (c.raw + 127) / 128;
+      const Seg c = take_block(a, work, p, tiles, run, unit, left, head, lane);
       const int64_t end = min((int64_t)tiles + 1, unit + left);
-      c.t_lo = (int)max(unit - 1, (int64_t)0);
-      c.N = (int)max(end - 1 - c.t_lo, (int64_t)0);
-      c.slot = unit <= 1 && end == tiles + 1 ? -1 : 2 * run + (unit <= 1);
-      if (head && lane == 0) {
-        First f;
-        f.row0 = c.row0;
-        f.h = c.h;
-        f.r0 = c.r0;
-        f.nr = c.nr;
-        f.pad = 0;
-        f.unit = unit;
-        f.units = tiles + 1;
-        work.first[run] = f;
-      }
       left -= end - unit;
       unit = 0;
       if (c.N > 0 || tiles == 0) {
@@ -746,9 +778,10 @@ __device__ __forceinline__ void store_part(const AttnArgs& a, const Work& work, 
 }
 inline size_t pad16(size_t n) { return (n + 15) & ~(size_t)15; }
 // The workspace for `runs` runs; with ws null only its size.
-inline size_t make_work(int runs, int G, int64_t max_new, void* ws, Work* w) {
-  const int64_t rows = max_new * G < 256 ? max_new * G : 256;
+inline size_t make_work(int runs, int block, int G, int64_t max_new, void* ws, Work* w) {
+  const int64_t rows = max_new * G < block ? max_new * G : block;
   const size_t head = 64, firsts = pad16(runs * sizeof(First)), states = pad16((size_t)2 * runs * rows * 4);
+  w->runs = runs;
   w->rows = (int)rows;
   char* p = reinterpret_cast<char*>(ws);
   w->cut = reinterpret_cast<Cut*>(p);
@@ -763,6 +796,7 @@ inline size_t make_work(int runs, int G, int64_t max_new, void* ws, Work* w) {
 // The merge of cut blocks after either kernel (attn_paged.cu).
 cudaError_t launch_merge(const AttnArgs& a, const Work& w, int runs, cudaStream_t s);
 // attn_wide.cu: the attention over pages expanded to fp16 tiles first, `tiles` bytes of them.
+cudaError_t launch_attn_narrow(const AttnArgs& a, const Work& w, int runs, cudaStream_t s);   // attn_narrow.cu
 size_t attn_wide_bytes(const AttnArgs& a);
 cudaError_t launch_attn_wide(const AttnArgs& a, const Work& w, int runs, void* tiles, cudaStream_t s);
 

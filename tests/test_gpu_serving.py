@@ -373,7 +373,8 @@ def test_attention_ragged(G, kw, q_dt, out_dt, causal):
     p.check_attention(q, scale, out, lse, counts, causal, out_dt)
 
 
-@pytest.mark.parametrize("n,L,G", [(1, 1, 4), (1, 5000, 4), (4, 4000, 4), (64, 2000, 2), (300, 300, 4), (33, 1300, 7)])
+@pytest.mark.parametrize("n,L,G", [(1, 1, 4), (1, 5000, 4), (4, 4000, 4), (64, 2000, 2), (300, 300, 4), (33, 1300, 7),
+                                   (3, 4600, 16), (16, 2500, 4), (17, 2500, 4), (5, 700, 3)])
 def test_attention_one_sequence(n, L, G):
     p = Paged(fmt(), 2, 1, 40, seed=40)
     p.fill([L])
@@ -410,6 +411,20 @@ def test_attention_many_short_sequences():
     q, scale, out, lse = p.attend(counts, 4, out_dt=BF16)
     assert int(p.status) == 0
     p.check_attention(q, scale, out, lse, counts, True, BF16)
+
+
+@pytest.mark.parametrize("G,kw,q_dt,out_dt", [(4, dict(n_sink=0), BF16, F32), (1, dict(src_dtype=F16), F16, F16),
+                                              (4, dict(k_rotate=1, n_sink=140), BF16, BF16),
+                                              (3, dict(src_dtype=F32), F32, F32)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_drafts(G, kw, q_dt, out_dt, causal):
+    # a few tokens per sequence: blocks of 16 rows, some full, some not, some sequences without any
+    p = Paged(fmt(**kw), 2, 6, 14, seed=60 + G)
+    p.fill([1700, 3, 129, 600, 260, 128])
+    counts = [5, 3, 0, 4, 1, 2]
+    q, scale, out, lse = p.attend(counts, G, q_dt, out_dt, causal)
+    assert int(p.status) == 0
+    p.check_attention(q, scale, out, lse, counts, causal, out_dt)
 
 
 def test_attention_rows_without_tokens_and_steep_scores():
