@@ -284,9 +284,36 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_narrow_kernel(const __gri
 #pragma unroll
             for (int e = 0; e < 4; ++e) st.o[k][n][e] = 0.0f;
 
-        // raw tiles: keys and values as fp16, 16 tokens at a time
+        // raw tiles of 16 tokens: keys and values as fp16
 #pragma unroll 1
-        for (int r0 = 128 * c.t_lo; r0 < min(128 * raw_end, c.raw); r0 += 16) {
+        for (int r0 = 16 * c.t_lo; r0 < 16 * raw_end; r0 += 16) {
+          // values: tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9, channels 8 g .. + 7 and 64 + 8 g .. + 7
+          uint32_t v[2][2][8];   // [token pair][channel half][channel]: (token, token + 1)
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              float y[2][8];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int r = r0 + 2 * t + 8 * u + e;
+                const bool sink = r < ns;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[e][j] = 0.0f;
+                if (r < c.raw)
+                  load8(sink ? a.sink[1] : a.res[1],
+                        (sink ? slab * a.b.n_sink + r : slab * a.b.res_cap + r - ns) * 128 + 64 * half + 8 * g, a.L.src_dtype,
+                        y[e]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  if (!(fabsf(y[e][j]) <= 65504.0f)) {
+                    flags |= isfinite(y[e][j]) ? KVQ_DEV_RANGE : KVQ_DEV_NONFINITE;
+                    y[e][j] = 0.0f;
+                  }
+              }
+#pragma unroll
+              for (int j = 0; j < 8; ++j) v[u][half][j] = pack_f16(y[0][j], y[1][j]);
+            }
           float acc[2][4] = {};
           {
             float x[2][32];
@@ -328,33 +355,6 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_narrow_kernel(const __gri
           const float none[4] = {0, 0, 0, 0}, one[2] = {1.0f, 1.0f}, zero[2] = {0.0f, 0.0f};
           uint32_t b[2][2];
           weigh(st, acc, cs, none, one, zero, zero, cols, true, g, b);
-          // values: tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9, channels 8 g .. + 7 and 64 + 8 g .. + 7
-          uint32_t v[2][2][8];   // [token pair][channel half][channel]: (token, token + 1)
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              float y[2][8];
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int r = r0 + 2 * t + 8 * u + e;
-                const bool sink = r < ns;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) y[e][j] = 0.0f;
-                if (r < c.raw)
-                  load8(sink ? a.sink[1] : a.res[1],
-                        (sink ? slab * a.b.n_sink + r : slab * a.b.res_cap + r - ns) * 128 + 64 * half + 8 * g, a.L.src_dtype,
-                        y[e]);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                  if (!(fabsf(y[e][j]) <= 65504.0f)) {
-                    flags |= isfinite(y[e][j]) ? KVQ_DEV_RANGE : KVQ_DEV_NONFINITE;
-                    y[e][j] = 0.0f;
-                  }
-              }
-#pragma unroll
-              for (int j = 0; j < 8; ++j) v[u][half][j] = pack_f16(y[0][j], y[1][j]);
-            }
 #pragma unroll
           for (int k = 0; k < 8; ++k)
 #pragma unroll

@@ -488,6 +488,7 @@ cudaError_t launch_attn_paged(const AttnArgs& args, cudaStream_t s) {
   Work w;
   const size_t small = make_work_for(a.G, a.b.max_rows, a.ws, &w, &runs);
   a.block = narrow(a.G, a.b.max_rows) ? 16 : 256;
+  a.raw_tile = a.block == 16 ? 16 : 128;
   if (a.block == 16) {
     const cudaError_t e = launch_attn_narrow(a, w, runs, s);
     return e != cudaSuccess ? e : launch_merge(a, w, runs, s);

@@ -72,7 +72,7 @@ __device__ __forceinline__ int seq_blocks(const AttnArgs& a, const AttnSeq& q) {
 }
 __device__ __forceinline__ int block_tiles(const AttnArgs& a, const AttnSeq& q, int b) {
   const Seen v = row_seen(a, q, (min(q.n * a.G, (b + 1) * a.block) - 1) / a.G);
-  return ((v.raw + 127) >> 7) + ((v.packed + 127) >> 7);
+  return (v.raw + a.raw_tile - 1) / a.raw_tile + ((v.packed + 127) >> 7);
 }
 
 // ---- the partition (one warp) ----------------------------------------------------------------
@@ -413,7 +413,7 @@ __device__ __forceinline__ Seg take_block(const AttnArgs& a, const Work& work, c
   const Seen last = row_seen(a, p.q, (c.r0 + c.nr - 1) / a.G);
   c.raw = last.raw;
   c.packed = last.packed;
-  c.n_raw = (c.raw + 127) / 128;
+  c.n_raw = (c.raw + a.raw_tile - 1) / a.raw_tile;
   const int64_t end = min((int64_t)tiles + 1, unit + left);
   c.t_lo = (int)max(unit - 1, (int64_t)0);
   c.N = (int)max(end - 1 - c.t_lo, (int64_t)0);

@@ -202,7 +202,7 @@ struct AttnArgs {
   int q_dtype, Hq, G;
   float qscale;             // softmax scale * log2 e
   int causal;
-  int block;                // query rows of a block of work (set by the launcher)
+  int block, raw_tile;      // query rows of a block of work, raw tokens of a tile (set by the launcher)
   void* out;
   int out_dtype;
   float* lse;
