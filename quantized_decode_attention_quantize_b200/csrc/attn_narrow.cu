@@ -35,7 +35,7 @@ constexpr size_t kSmem = (size_t)kWarps * kStages * kStage + sizeof(Small);
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -409,12 +409,15 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_narrow_kernel(const __gri
             edge |= cols[q] < 128;
           }
           edge = __any_sync(0xffffffffu, edge);
-#pragma unroll 2
-          for (int k0 = 0; k0 < 8; ++k0) {
-            float acc[2][4] = {};
+          // the next 16 tokens' scores are under way while these are weighed
+          auto scores = [&](int k0, float (&acc)[2][4]) {
             const uint4 ka = reinterpret_cast<const uint4*>(in)[(16 * k0 + g) * 4 + t];
             const uint4 kb = reinterpret_cast<const uint4*>(in)[(16 * k0 + g + 8) * 4 + t];
             const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[n][e] = 0.0f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const uint32_t ua = wa[k] >> 8, ub = wb[k] >> 8;
@@ -426,6 +429,16 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_narrow_kernel(const __gri
                          bs[n][4 * k + 3]);
               }
             }
+          };
+          float acc[2][4], ahead[2][4];
+          scores(0, ahead);
+#pragma unroll 1
+          for (int k0 = 0; k0 < 8; ++k0) {
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[n][e] = ahead[n][e];
+            if (k0 < 7) scores(k0 + 1, ahead);
             const __half* vs = reinterpret_cast<const __half*>(in + kVMeta) + 16 * k0 + g;
             float s[2], ls[2], z[2];
             int left[4];

@@ -433,19 +433,27 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const __grid_constant__
   auto slot = [&](int z) { return (int64_t)(z == 0 ? 2 * run - 1 : 2 * (run + z - 1)) * work.rows; };
   for (int r = warp + 8 * blockIdx.y; r < f.nr; r += 8 * gridDim.y) {
     const int64_t row = (f.row0 + (f.r0 + r) / a.G) * a.Hq + f.h * a.G + (f.r0 + r) % a.G;
-    float m = -INFINITY;
-    for (int z = 0; z < parts; ++z) m = fmaxf(m, work.m[slot(z) + r]);
-    float l = 0.0f, o[4] = {0, 0, 0, 0};
-    for (int z = 0; z < parts; ++z) {
-      const float mz = work.m[slot(z) + r];
-      if (mz == -INFINITY) continue;
-      const float g = exp2_approx(mz - m);
-      l += g * work.l[slot(z) + r];
-      const float4 v = *reinterpret_cast<const float4*>(work.o + (slot(z) + r) * 128 + 4 * lane);
-      o[0] += g * v.x;
-      o[1] += g * v.y;
-      o[2] += g * v.z;
-      o[3] += g * v.w;
+    // states 32 parts at a time, a lane each; then their rows, several in flight
+    float m = -INFINITY, l = 0.0f, o[4] = {0, 0, 0, 0};
+    for (int z0 = 0; z0 < parts; z0 += 32) {
+      const bool there = z0 + lane < parts;
+      const float mz = there ? work.m[slot(z0 + lane) + r] : -INFINITY, lz = there ? work.l[slot(z0 + lane) + r] : 0.0f;
+      const float top = fmaxf(m, warp_max(mz)), f = m == -INFINITY ? 0.0f : exp2_approx(m - top);
+      const float gz = mz == -INFINITY ? 0.0f : exp2_approx(mz - top);
+      m = top;
+      l = l * f + warp_sum(gz * lz);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] *= f;
+      const int n = min(32, parts - z0);
+#pragma unroll 8
+      for (int z = 0; z < n; ++z) {
+        const float g = __shfl_sync(0xffffffffu, gz, z);
+        const float4 v = *reinterpret_cast<const float4*>(work.o + (slot(z0 + z) + r) * 128 + 4 * lane);
+        o[0] = fmaf(g, v.x, o[0]);
+        o[1] = fmaf(g, v.y, o[1]);
+        o[2] = fmaf(g, v.z, o[2]);
+        o[3] = fmaf(g, v.w, o[3]);
+      }
     }
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
