@@ -471,10 +471,10 @@ cudaError_t launch_merge(const AttnArgs& a, const Work& w, int runs, cudaStream_
 }
 }  // namespace attn
 
-// Expanding the pages first pays when several row blocks read each of them: measured at 2048 tokens x 4
-// heads over 16k, 32 row blocks, and at one and two row blocks per sequence (see the notes at
-// attn_wide_kernel).
-bool attn_wide_pays(int num_seqs, int G, int64_t n_rows) { return n_rows * G >= (int64_t)num_seqs * 512; }
+// Expanding the pages first pays from more than one row block (256 rows) per sequence on.  Measured, us, without
+// / with: 64 tokens x 4 heads (one block) over 18k 78 / 113; 13 ragged chunks of 285 rows over 4k, 32 heads
+// 605 / 518; 2048 tokens x 4 heads over 16k 900 / 690 when both were first built.
+bool attn_wide_pays(int num_seqs, int G, int64_t n_rows) { return n_rows * G > (int64_t)num_seqs * 256; }
 
 // Blocks of 16 rows, a warp each, up to 64 rows a sequence; blocks of 256 on the whole CTA above.
 constexpr int kNarrowRows = 64, kNarrowWarps = 8;

@@ -177,6 +177,7 @@ struct AppendArgs {
   const int32_t* positions;
   int32_t* t_quant_out;
   int32_t* t_res_out;
+  int direct;               // sequence = unit (set by the launcher)
   void* sink[2];
   void* res[2];
   int32_t* status;

@@ -51,38 +51,105 @@ __device__ __forceinline__ AppendSeq append_seq(const PagedBatch& b, int s) {
   return q;
 }
 
-// A token's octet of keys or values on its way in: new row `row` (turned and rounded when it
-// is a key).
-__device__ __forceinline__ void new_octet(const AppendArgs& a, int which, int64_t row, int h, int o, int64_t pos,
-                                          float (&x)[8], int& flags) {
-  const int64_t base = row * a.st[which] + h * a.sh[which];
-  load8(a.src[which], base + 8 * o, a.L.src_dtype, x);
-  float fin = 0.0f;
+// An octet of a row as its source type holds it (fp32: eight words, else four).
+template <int DT>
+struct Octet {
+  uint32_t w[DT == KVQ_F32 ? 8 : 4];
+};
+template <int DT>
+__device__ __forceinline__ Octet<DT> octet_load(const void* base, int64_t i) {
+  Octet<DT> x;
+  const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(base) + i * (DT == KVQ_F32 ? 4 : 2));
 #pragma unroll
-  for (int j = 0; j < 8; ++j) fin = fmaf(x[j], 0.0f, fin);
-  if (!(fin == 0.0f)) flags |= KVQ_DEV_NONFINITE;
-  if (which == KVQ_KEYS && a.rope.table && 8 * o < a.rope.rot) {
-    if (a.positions) pos = a.positions[row];
-    if (pos < 0 || pos >= a.rope.n_pos) {
+  for (int k = 0; k < (DT == KVQ_F32 ? 2 : 1); ++k) {
+    const uint4 v = p[k];
+    x.w[4 * k] = v.x; x.w[4 * k + 1] = v.y; x.w[4 * k + 2] = v.z; x.w[4 * k + 3] = v.w;
+  }
+  return x;
+}
+template <int DT>
+__device__ __forceinline__ void octet_store(void* base, int64_t i, const Octet<DT>& x) {
+  uint4* p = reinterpret_cast<uint4*>(reinterpret_cast<char*>(base) + i * (DT == KVQ_F32 ? 4 : 2));
+#pragma unroll
+  for (int k = 0; k < (DT == KVQ_F32 ? 2 : 1); ++k) p[k] = make_uint4(x.w[4 * k], x.w[4 * k + 1], x.w[4 * k + 2], x.w[4 * k + 3]);
+}
+template <int DT>
+__device__ __forceinline__ void octet_get(const Octet<DT>& x, float (&f)[8]) {
+  if constexpr (DT == KVQ_F32) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(x.w[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (DT == KVQ_F16) {
+        f[2 * j] = half_bits_to_float((uint16_t)(x.w[j] & 0xffffu));
+        f[2 * j + 1] = half_bits_to_float((uint16_t)(x.w[j] >> 16));
+      } else {
+        f[2 * j] = __uint_as_float(x.w[j] << 16);
+        f[2 * j + 1] = __uint_as_float(x.w[j] & 0xffff0000u);
+      }
+    }
+  }
+}
+template <int DT>
+__device__ __forceinline__ Octet<DT> octet_put(const float (&f)[8]) {   // rounded to the type
+  Octet<DT> x;
+  if constexpr (DT == KVQ_F32) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x.w[j] = __float_as_uint(f[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x.w[j] = pack2(f[2 * j], f[2 * j + 1], DT);
+  }
+  return x;
+}
+
+// Octet o of N rows, those with fresh[k] being new tokens (row `row[k]` of the source, at position pos[k]),
+// checked, and when they are keys turned and rounded.  The 16 lanes of a row call together: the
+// half-layout partner comes from its lane.
+template <int DT, int N>
+__device__ __forceinline__ void turn_rows(const AppendArgs& a, int which, int o, const int64_t (&row)[N],
+                                          const int64_t (&pos)[N], const bool (&fresh)[N], Octet<DT> (&x)[N], int& flags) {
+  const bool turns = which == KVQ_KEYS && a.rope.table;
+  const int po = rope_partner(a.rope, o);
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    Octet<DT> y = x[k];
+    if (turns && !a.rope.inter) {
+#pragma unroll
+      for (int j = 0; j < (DT == KVQ_F32 ? 8 : 4); ++j) y.w[j] = __shfl_sync(0xffffffffu, x[k].w[j], po, 16);
+    }
+    if (!fresh[k]) continue;
+    float f[8], fin = 0.0f;
+    octet_get<DT>(x[k], f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) fin = fmaf(f[j], 0.0f, fin);
+    if (!(fin == 0.0f)) flags |= KVQ_DEV_NONFINITE;
+    if (!turns || 8 * o >= a.rope.rot) continue;
+    const int64_t at = a.positions ? a.positions[row[k]] : pos[k];
+    if (at < 0 || at >= a.rope.n_pos) {
       flags |= KVQ_DEV_BOUNDS;
-      return;
+      continue;
     }
     float p[8];
-    const int po = rope_partner(a.rope, o);
-    load8(a.src[which], base + 8 * po, a.L.src_dtype, p);
+    octet_get<DT>(y, p);
     OctetTurn t;
-    rope_load(a.rope, pos, o, t);
-    rope_turn(a.rope, o, t, x, p);
-    round8(x, a.L.src_dtype);
+    rope_load(a.rope, at, o, t);
+    rope_turn(a.rope, o, t, f, p);
+    x[k] = octet_put<DT>(f);
   }
 }
 
 // Grid (units, kv head x {keys, values}).  Thread (r, o): octet o = t % 16 of rows
-// 2 (r + 16 j), 2 (r + 16 j) + 1, j = 0 .. 3, of the unit's 128 rows, in registers from the
-// load to the codes.  Keys: a channel's min and max meet over the two row slices of a warp,
-// then over the 8 warps in shared memory; values: a token's over its 16 lanes.  The rows of a
-// value pair sit in one thread, which owns the pair's word.
-__global__ void __launch_bounds__(kThreads) append_paged_kernel(const __grid_constant__ AppendArgs a) {
+// 2 (r + 16 j), 2 (r + 16 j) + 1, j = 0 .. 3, of the unit's 128 rows, in registers (as the source type holds
+// them; a rotating format's keys in fp32) from the load to the codes.  Keys: a channel's min and max meet over
+// the two row slices of a warp, then over the 8 warps in shared memory; values: a token's over its 16
+// lanes.  The rows of a value pair sit in one thread, which owns the pair's word.
+// Bound by memory: the new rows once in, codes or raw rows once out.  Rows kept as loaded leave two CTAs per SM
+// where fp32 registers left one.
+template <int DT, bool ROT>
+__global__ void __launch_bounds__(kThreads, DT == KVQ_F32 || ROT ? 1 : 2)
+    append_paged_kernel(const __grid_constant__ AppendArgs a) {
   __shared__ float pmin[8][128], pmax[8][128];
   __shared__ float sf[128], zf[128], rf[128];
   griddep_wait();
@@ -90,7 +157,12 @@ __global__ void __launch_bounds__(kThreads) append_paged_kernel(const __grid_con
   const PagedBatch& b = a.b;
   const int h = blockIdx.y >> 1, which = blockIdx.y & 1;
   int s, unit;
-  if (!find_unit(b.num_seqs, blockIdx.x, [&](int i) { return append_seq(b, i).units; }, &s, &unit)) return;
+  if (a.direct) {   // one unit each: no search
+    s = blockIdx.x;
+    unit = 0;
+  } else if (!find_unit(b.num_seqs, blockIdx.x, [&](int i) { return append_seq(b, i).units; }, &s, &unit)) {
+    return;
+  }
   AppendSeq q = append_seq(b, s);
   int flags = q.ok ? 0 : KVQ_DEV_BOUNDS;
   // every block the sequence needs is checked by each of its CTAs: all of it or nothing
@@ -111,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) append_paged_kernel(const __grid_con
     if (flags && threadIdx.x == 0) flag(a.status, flags);
     return;
   }
-  const int dt = a.L.src_dtype, ns = b.n_sink;
+  const int ns = b.n_sink;
   const int o = threadIdx.x & 15, rs = threadIdx.x >> 4, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t pos0 = (int64_t)ns + q.tq + q.tr;                 // position of the first new token
   const int64_t slab = (int64_t)s * a.L.Hkv + h;
@@ -119,13 +191,42 @@ __global__ void __launch_bounds__(kThreads) append_paged_kernel(const __grid_con
   // row r of (window rows, then new tokens behind the sink)
   const int64_t new0 = q.row0 + q.to_sink - q.old;                // + r: the new row of r >= old
   const int64_t npos = pos0 + q.to_sink - q.old;                  // + r: its position
-  float x[8][8];
-  if (q.groups > 0) {
+  // new rows [lo, hi) (counted from source row `from` at position `at`) to rows from `to` on of a raw array, four
+  // of this thread's in flight
+  auto copy_rows = [&](int64_t from, int64_t at, int lo, int hi, char* dst, int to) {
+    for (int r0 = lo; r0 < hi; r0 += 64) {
+      Octet<DT> x[4] = {};
+      int64_t row[4], pos[4];
+      bool fresh[4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int r = 128 * unit + 2 * (rs + 16 * (k >> 1)) + (k & 1);
-      if (r < q.old) load8(res, (int64_t)r * 128 + 8 * o, dt, x[k]);
-      else new_octet(a, which, new0 + r, h, o, npos + r, x[k], flags);
+      for (int k = 0; k < 4; ++k) {
+        const int r = r0 + rs + 16 * k;
+        fresh[k] = r < hi;
+        row[k] = from + r;
+        pos[k] = at + r;
+        if (fresh[k]) x[k] = octet_load<DT>(a.src[which], row[k] * a.st[which] + h * a.sh[which] + 8 * o);
+      }
+      turn_rows<DT, 4>(a, which, o, row, pos, fresh, x, flags);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (fresh[k]) octet_store<DT>(dst, (int64_t)(to + r0 - lo + rs + 16 * k) * 128 + 8 * o, x[k]);
+    }
+  };
+  if (q.groups > 0) {
+    Octet<DT> raw[8];
+    {
+      int64_t row[8], pos[8];
+      bool fresh[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int r = 128 * unit + 2 * (rs + 16 * (k >> 1)) + (k & 1);
+        fresh[k] = r >= q.old;
+        row[k] = new0 + r;
+        pos[k] = npos + r;
+        raw[k] = fresh[k] ? octet_load<DT>(a.src[which], row[k] * a.st[which] + h * a.sh[which] + 8 * o)
+                          : octet_load<DT>(res, (int64_t)r * 128 + 8 * o);
+      }
+      turn_rows<DT, 8>(a, which, o, row, pos, fresh, raw, flags);
     }
     const int blk = b.table[(int64_t)s * b.max_blocks + q.tq / 128 + unit];
     const Side& S = a.L.side[which];
@@ -134,23 +235,40 @@ __global__ void __launch_bounds__(kThreads) append_paged_kernel(const __grid_con
     __half* scale = reinterpret_cast<__half*>(S.scale) + ps * 128;
     __half* zero = reinterpret_cast<__half*>(S.zero) + ps * 128;
     if (which == KVQ_KEYS) {
-      if (a.L.k_rotate) {
+      float wide[ROT ? 8 : 1][8];
+      if constexpr (ROT) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          wht128_octet_unscaled(x[k], lane);
+          octet_get<DT>(raw[k], wide[k]);
+          wht128_octet_unscaled(wide[k], lane);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[k][j] = __fmul_rn(x[k][j], a.L.rot_scale);
+          for (int j = 0; j < 8; ++j) wide[k][j] = __fmul_rn(wide[k][j], a.L.rot_scale);
         }
       }
+      auto value = [&](int k, float (&x)[8]) {
+        if constexpr (ROT) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = wide[k][j];
+        } else {
+          octet_get<DT>(raw[k], x);
+        }
+      };
       float mn[8], mx[8];
+      value(0, mn);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) mx[j] = mn[j];
+#pragma unroll
+      for (int k = 1; k < 8; ++k) {
+        float x[8];
+        value(k, x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          mn[j] = fminf(mn[j], x[j]);
+          mx[j] = fmaxf(mx[j], x[j]);
+        }
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        mn[j] = mx[j] = x[0][j];
-#pragma unroll
-        for (int k = 1; k < 8; ++k) {
-          mn[j] = fminf(mn[j], x[k][j]);
-          mx[j] = fmaxf(mx[j], x[k][j]);
-        }
         mn[j] = fminf(mn[j], __shfl_xor_sync(0xffffffffu, mn[j], 16));
         mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 16));
         if (lane < 16) {
@@ -186,17 +304,21 @@ __global__ void __launch_bounds__(kThreads) append_paged_kernel(const __grid_con
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int r = 2 * (rs + 16 * (k >> 1)) + (k & 1);
-        *reinterpret_cast<uint32_t*>(codes + r * 64 + 4 * o) = pack8(x[k], s8, r8, z8, 4).x;
+        float x[8];
+        value(k, x);
+        *reinterpret_cast<uint32_t*>(codes + r * 64 + 4 * o) = pack8(x, s8, r8, z8, 4).x;
       }
     } else {
       uint32_t half_word = 0;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        float mn = x[k][0], mx = x[k][0];
+        float x[8];
+        octet_get<DT>(raw[k], x);
+        float mn = x[0], mx = x[0];
 #pragma unroll
         for (int j = 1; j < 8; ++j) {
-          mn = fminf(mn, x[k][j]);
-          mx = fmaxf(mx, x[k][j]);
+          mn = fminf(mn, x[j]);
+          mx = fmaxf(mx, x[j]);
         }
 #pragma unroll
         for (int m = 1; m < 16; m <<= 1) {
@@ -217,7 +339,7 @@ __global__ void __launch_bounds__(kThreads) append_paged_kernel(const __grid_con
           z8[j] = __half2float(zh);
           r8[j] = __frcp_rn(s8[j]);
         }
-        const uint32_t w = pack8(x[k], s8, r8, z8, 2).x & 0xffffu;
+        const uint32_t w = pack8(x, s8, r8, z8, 2).x & 0xffffu;
         if ((k & 1) == 0) half_word = w;
         else reinterpret_cast<uint32_t*>(codes)[u * 16 + o] = half_word | (w << 16);
       }
@@ -225,30 +347,19 @@ __global__ void __launch_bounds__(kThreads) append_paged_kernel(const __grid_con
   }
   if (unit == 0) {
     // the sink's share of the new tokens
-    char* sink = reinterpret_cast<char*>(a.sink[which]) + slab * ns * 128 * a.L.raw_bytes;
-    for (int i = rs; i < q.to_sink; i += 16) {
-      float y[8];
-      new_octet(a, which, q.row0 + i, h, o, pos0 + i, y, flags);
-      store8(sink, (int64_t)(ns + q.tr + i) * 128 + 8 * o, dt, y);
-    }
+    if (q.to_sink > 0)
+      copy_rows(q.row0, pos0, 0, q.to_sink, reinterpret_cast<char*>(a.sink[which]) + slab * ns * 128 * a.L.raw_bytes,
+                ns + q.tr);
     // rows behind the packed groups start the window anew; every thread has read its window
     // rows of group 0 (the only ones that overlap rows below 128) before the barrier
     if (q.groups > 0) {
       __syncthreads();
-      for (int r = rs; r < q.total - 128 * q.groups; r += 16) {
-        float y[8];
-        new_octet(a, which, new0 + 128 * q.groups + r, h, o, npos + 128 * q.groups + r, y, flags);
-        store8(res, (int64_t)r * 128 + 8 * o, dt, y);
-      }
+      copy_rows(new0, npos, 128 * q.groups, q.total, res, 0);
     }
   }
   if (q.groups == 0) {
     const int lo = max(q.old, (q.old / 128 + unit) * 128), hi = min(q.total, (q.old / 128 + unit + 1) * 128);
-    for (int r = lo + rs; r < hi; r += 16) {
-      float y[8];
-      new_octet(a, which, new0 + r, h, o, npos + r, y, flags);
-      store8(res, (int64_t)r * 128 + 8 * o, dt, y);
-    }
+    copy_rows(new0, npos, lo, hi, res, lo);
   }
   flags = __reduce_or_sync(0xffffffffu, flags);
   if (flags && lane == 0) flag(a.status, flags);
@@ -282,8 +393,10 @@ __device__ __forceinline__ ReadSeq read_seq(const ReadArgs& a, int s) {
   return q;
 }
 
-// Grid (units, kv head x {keys, values}); threads as in the append.
-__global__ void __launch_bounds__(kThreads) read_paged_kernel(const __grid_constant__ ReadArgs a) {
+// Grid (units, kv head x {keys, values}); thread (r, o): octet o of rows r + 16 j (keys) or pairs r + 16 j
+// (values).  Bound by the rows written.
+template <int OD>
+__global__ void __launch_bounds__(kThreads, 4) read_paged_kernel(const __grid_constant__ ReadArgs a) {
   griddep_wait();
   griddep_launch_dependents();
   const PagedBatch& b = a.b;
@@ -307,10 +420,11 @@ __global__ void __launch_bounds__(kThreads) read_paged_kernel(const __grid_const
                       slab * (win ? b.res_cap : ns) * 128 * a.L.raw_bytes;
     const int64_t base = win ? (int64_t)ns + q.tq : 0;
     const int64_t lo = max(q.p0, base), hi = win ? q.p1 : min(q.p1, (int64_t)ns);
+#pragma unroll 4
     for (int64_t p = lo + rs; p < hi; p += 16) {
       float x[8];
       load8(src, (p - base) * 128 + 8 * o, dt, x);
-      store8(a.out[which], at(p), a.out_dtype, x);
+      store8(a.out[which], at(p), OD, x);
     }
     return;
   }
@@ -327,52 +441,73 @@ __global__ void __launch_bounds__(kThreads) read_paged_kernel(const __grid_const
   const uint8_t* codes = reinterpret_cast<const uint8_t*>(S.codes) + ps * S.code_slab_bytes;
   const __half* scale = reinterpret_cast<const __half*>(S.scale) + ps * 128;
   const __half* zero = reinterpret_cast<const __half*>(S.zero) + ps * 128;
+  // all of the thread's words of the group first, then the rows
   if (which == KVQ_KEYS) {
     float s8[8], z8[8];
     load8(scale, 8 * o, KVQ_F16, s8);
     load8(zero, 8 * o, KVQ_F16, z8);
-    for (int r = (lo & ~15) + rs; r < ((hi + 15) & ~15); r += 16) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + r * 64 + 4 * o);
+    uint32_t w[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k] = reinterpret_cast<const uint32_t*>(codes)[(rs + 16 * k) * 16 + o];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int r = rs + 16 * k;
       float x[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = __fadd_rn(__fmul_rn((float)((w >> (4 * j)) & 15u), s8[j]), z8[j]);
+      for (int j = 0; j < 8; ++j) x[j] = __fadd_rn(__fmul_rn((float)((w[k] >> (4 * j)) & 15u), s8[j]), z8[j]);
       if (a.L.k_rotate) {
         wht128_octet_unscaled(x, lane);
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(x[j], a.L.rot_scale);
       }
-      if (r >= lo && r < hi) store8(a.out[which], at(base + r), a.out_dtype, x);
+      if (r >= lo && r < hi) store8(a.out[which], at(base + r), OD, x);
     }
   } else {
-    for (int u = lo / 2 + rs; 2 * u < hi; u += 16) {
-      const uint32_t w = reinterpret_cast<const uint32_t*>(codes)[u * 16 + o];
+    uint32_t w[4], sz[4][2];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int u = rs + 16 * k;
+      w[k] = reinterpret_cast<const uint32_t*>(codes)[u * 16 + o];
+      sz[k][0] = reinterpret_cast<const uint32_t*>(scale)[u];
+      sz[k][1] = reinterpret_cast<const uint32_t*>(zero)[u];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = 2 * u + e;
-        if (r < lo || r >= hi) continue;
-        const float sv = __half2float(scale[r]), zv = __half2float(zero[r]);
+        const int r = 2 * (rs + 16 * k) + e;
+        const float sv = half_bits_to_float((uint16_t)(sz[k][0] >> (16 * e))), zv = half_bits_to_float((uint16_t)(sz[k][1] >> (16 * e)));
         float x[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          x[j] = __fadd_rn(__fmul_rn((float)((w >> (16 * e + 2 * j)) & 3u), sv), zv);
-        store8(a.out[which], at(base + r), a.out_dtype, x);
+        for (int j = 0; j < 8; ++j) x[j] = __fadd_rn(__fmul_rn((float)((w[k] >> (16 * e + 2 * j)) & 3u), sv), zv);
+        if (r >= lo && r < hi) store8(a.out[which], at(base + r), OD, x);
       }
-    }
   }
 }
 
 }  // namespace
 
-cudaError_t launch_append_paged(const AppendArgs& a, cudaStream_t s) {
-  // units of a sequence: at most floor((res_cap + n) / 128), one at least
-  const int64_t units = (int64_t)a.b.num_seqs * (a.b.res_cap / 128) + a.b.n_rows / 128;
-  return launch_pdl(append_paged_kernel, dim3((unsigned)units, 2 * a.L.Hkv), dim3(kThreads), 0, s, a);
+cudaError_t launch_append_paged(const AppendArgs& args, cudaStream_t s) {
+  // units of a sequence: at most floor((res_cap + n) / 128), one at least; exactly one each for short
+  // appends to a window of one group, which then need no search for their sequence
+  const int64_t units = (int64_t)args.b.num_seqs * (args.b.res_cap / 128) + args.b.n_rows / 128;
+  AppendArgs a = args;
+  a.direct = a.b.res_cap == 128 && a.b.max_rows < 128;
+  const dim3 grid(a.direct ? a.b.num_seqs : (unsigned)units, 2 * a.L.Hkv);
+  const bool rot = a.L.k_rotate;
+  auto kern = a.L.src_dtype == KVQ_F32   ? (rot ? append_paged_kernel<KVQ_F32, true> : append_paged_kernel<KVQ_F32, false>)
+              : a.L.src_dtype == KVQ_F16 ? (rot ? append_paged_kernel<KVQ_F16, true> : append_paged_kernel<KVQ_F16, false>)
+                                         : (rot ? append_paged_kernel<KVQ_BF16, true> : append_paged_kernel<KVQ_BF16, false>);
+  return launch_pdl(kern, grid, dim3(kThreads), 0, s, a);
 }
 
 cudaError_t launch_read_paged(const ReadArgs& a, cudaStream_t s) {
   // touched groups of n rows: at most n / 128 + 2; the sink and the window two more
   const int64_t units = 4ll * a.b.num_seqs + a.b.n_rows / 128;
-  return launch_pdl(read_paged_kernel, dim3((unsigned)units, 2 * a.L.Hkv), dim3(kThreads), 0, s, a);
+  auto kern = a.out_dtype == KVQ_F32   ? read_paged_kernel<KVQ_F32>
+              : a.out_dtype == KVQ_F16 ? read_paged_kernel<KVQ_F16>
+                                       : read_paged_kernel<KVQ_BF16>;
+  return launch_pdl(kern, dim3((unsigned)units, 2 * a.L.Hkv), dim3(kThreads), 0, s, a);
 }
 
 }  // namespace kvq
