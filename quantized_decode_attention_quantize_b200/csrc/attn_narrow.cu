@@ -4,7 +4,7 @@
 // Mathematics.  Scores are products with tokens as M and query rows as N (m16n8k16, two of them for 16
 // rows), values with channels as M and query rows as N:
 //   A[t][d] = c[t][d] 2^-24 f_d   (a 4-bit code masked into the low bits of an fp16 number, f_d = 1 or 16),
-//   B[d][r] = fp16(q[r][d] s[d] / f_d)  per group,   score = 2^24 (A B) + sum_d q z,
+//   B[d][r] = fp16(q[r][d] s[d] / f_d)  per group,   score = 2^24 (A B) + sum_d (q z + 8 (q s - f_d B)),
 //   A[d][t] = c[t][d] exactly (masked into 2^k + c, less 2^k),   B[t][r] = fp16(p s 2^7),
 //   O[d][r] = 2^-7 (A B) + sum_t p z.
 // A lane's four words of a key row are the A fragments of eight k-steps (channels go to k in the order that the
@@ -383,13 +383,17 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_narrow_kernel(const __gri
             const uint32_t zq[4] = {lo2(z.x, z.z), hi2(z.x, z.z), lo2(z.y, z.w), hi2(z.y, z.w)};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const float2 zf = h2f(zq[j]);
+              const float2 zf = h2f(zq[j]), sf = h2f(sp[j]);
               const float f = j & 1 ? 16.0f : 1.0f;
 #pragma unroll
               for (int n = 0; n < 2; ++n) {
                 const float2 qf = h2f(qp[n][4 * k + j]);
                 bs[n][4 * k + j] = h2mul(qp[n][4 * k + j], sp[j]);
-                zd[n] = fmaf(qf.x * f, zf.x, fmaf(qf.y * f, zf.y, zd[n]));
+                // q z, and what the rounding of q s takes from a code of 8, so that the error goes with c - 8
+                const float2 bf = h2f(bs[n][4 * k + j]);
+                const float ex = fmaf(8.0f, fmaf(qf.x, sf.x, -bf.x), qf.x * zf.x);
+                const float ey = fmaf(8.0f, fmaf(qf.y, sf.y, -bf.y), qf.y * zf.y);
+                zd[n] = fmaf(f, ex + ey, zd[n]);
               }
             }
           }

@@ -104,6 +104,37 @@ __device__ __forceinline__ Octet<DT> octet_put(const float (&f)[8]) {   // round
   return x;
 }
 
+// Codes of eight values, BITS each, packed from the low end: rint_even(fl(fl(x - z) / s)) as pack8 finds it (the
+// product with fl(1 / s) decides unless it lies within 2^-12 of a half-integer).  0 <= x - z and s is rounded
+// up, so the quotient stays within half a step of 0 .. 2^BITS - 1 and needs no clamp.  q + 1.5 * 2^23 holds
+// the integer in its low bits; the sums of these words, less the constants, are the packed codes.
+template <int BITS>
+__device__ __forceinline__ uint32_t pack_codes(const float (&x)[8], const float (&s)[8], const float (&rs)[8],
+                                               const float (&z)[8]) {
+  const float big = 12582912.0f;
+  float q[8], t[8];
+  bool near = false;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    q[j] = __fmul_rn(__fsub_rn(x[j], z[j]), rs[j]);
+    t[j] = __fadd_rn(q[j], big);
+    near |= fabsf(__fsub_rn(q[j], __fsub_rn(t[j], big))) > 0.5f - 0x1p-12f;
+  }
+  if (near) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (fabsf(__fsub_rn(q[j], __fsub_rn(t[j], big))) > 0.5f - 0x1p-12f)
+        t[j] = __fadd_rn(__fdiv_rn(__fsub_rn(x[j], z[j]), s[j]), big);
+  }
+  uint32_t w = 0, less = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    w += __float_as_uint(t[j]) << (BITS * j);
+    less += 0x4B400000u << (BITS * j);
+  }
+  return w - less;
+}
+
 // Octet o of N rows, those with fresh[k] being new tokens (row `row[k]` of the source, at position pos[k]),
 // checked, and when they are keys turned and rounded.  The 16 lanes of a row call together: the
 // half-layout partner comes from its lane.
@@ -306,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, DT == KVQ_F32 || ROT ? 1 : 2)
         const int r = 2 * (rs + 16 * (k >> 1)) + (k & 1);
         float x[8];
         value(k, x);
-        *reinterpret_cast<uint32_t*>(codes + r * 64 + 4 * o) = pack8(x, s8, r8, z8, 4).x;
+        *reinterpret_cast<uint32_t*>(codes + r * 64 + 4 * o) = pack_codes<4>(x, s8, r8, z8);
       }
     } else {
       uint32_t half_word = 0;
@@ -339,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, DT == KVQ_F32 || ROT ? 1 : 2)
           z8[j] = __half2float(zh);
           r8[j] = __frcp_rn(s8[j]);
         }
-        const uint32_t w = pack8(x, s8, r8, z8, 2).x & 0xffffu;
+        const uint32_t w = pack_codes<2>(x, s8, r8, z8) & 0xffffu;
         if ((k & 1) == 0) half_word = w;
         else reinterpret_cast<uint32_t*>(codes)[u * 16 + o] = half_word | (w << 16);
       }

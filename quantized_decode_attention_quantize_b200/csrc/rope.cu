@@ -50,7 +50,7 @@ struct NormArgs {
   HeadRows side[2];
   int D, dtype;
   int64_t n_tokens;
-  float eps, offset;
+  float eps, offset, inv_d;
   RopeArgs rope;
   const int32_t* positions;
   int32_t* status;
@@ -58,17 +58,17 @@ struct NormArgs {
 
 // kHeads heads of one token and side per group of lanes: all their loads are issued first, and the token's
 // cosines and sines are read once for them.
-constexpr int kHeads = 4;
+constexpr int kHeads = 2;
 
 template <int LPR, int DT>
-__global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(256, 4) norm_rope_kernel(const __grid_constant__ NormArgs a) {
   griddep_wait();
   griddep_launch_dependents();
   const int cq = (a.side[0].heads + kHeads - 1) / kHeads, chunks = cq + (a.side[1].heads + kHeads - 1) / kHeads;
-  const int64_t item = (int64_t)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
+  const unsigned item = blockIdx.x * (256 / LPR) + threadIdx.x / LPR;   // the host keeps rows below 2^31
   const int o = threadIdx.x % LPR;
-  const int64_t t = item / chunks;
-  const int chunk = (int)(item - t * chunks), which = chunk >= cq;
+  const int64_t t = item / (unsigned)chunks;
+  const int chunk = (int)(item - (unsigned)t * chunks), which = chunk >= cq;
   const HeadRows& S = a.side[which];
   const int h0 = (which ? chunk - cq : chunk) * kHeads;
   const bool live = t < a.n_tokens && 8 * o < a.D;
@@ -93,26 +93,35 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ 
     }
   }
   float w[8];
-  if (S.weight && live) load8(S.weight, 8 * o, DT, w);
+  if (S.weight) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = 0.0f;
+    if (live) load8(S.weight, 8 * o, DT, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] += a.offset;
+  }
   const int po = rope_partner(a.rope, o);
-  float fin = 0.0f;
+  bool bad = false;
 #pragma unroll
   for (int k = 0; k < kHeads; ++k) {
     float ss = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      fin = fmaf(x[k][j], 0.0f, fin);
-      ss = fmaf(x[k][j], x[k][j], ss);
+    for (int j = 0; j < 8; ++j) ss = fmaf(x[k][j], x[k][j], ss);
+    if (!(ss <= 3.402823466e38f)) {   // a NaN or Inf among them, or squares that overflow
+#pragma unroll
+      for (int j = 0; j < 8; ++j) bad |= !isfinite(x[k][j]);
     }
     if (S.weight) {   // alike over the lanes of a row; rows of one warp may differ
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[k][j] = live ? x[k][j] * (a.offset + w[j]) : 0.0f;
+      for (int j = 0; j < 8; ++j) x[k][j] *= w[j];
     }
 #pragma unroll
     for (int m = 1; m < LPR; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-    const float r = S.weight ? 1.0f / sqrtf(ss / (float)a.D + a.eps) : 1.0f;
+    if (S.weight) {
+      const float r = rsqrtf(fmaf(ss, a.inv_d, a.eps));
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[k][j] *= r;
+      for (int j = 0; j < 8; ++j) x[k][j] *= r;
+    }
     if (a.rope.table) {
       float p[8];
       if (!a.rope.inter) {
@@ -123,7 +132,7 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ 
     }
     if (k < n) store8(S.y, t * S.yt + (h0 + k) * S.yh + 8 * o, DT, x[k]);
   }
-  if (!(fin == 0.0f)) flag(a.status, KVQ_DEV_NONFINITE);
+  if (bad) flag(a.status, KVQ_DEV_NONFINITE);
 }
 
 template <int LPR>
@@ -163,6 +172,7 @@ cudaError_t launch_norm_rope(int D, int dtype, int64_t n_tokens, const HeadRows&
   a.n_tokens = n_tokens;
   a.eps = eps;
   a.offset = weight_offset;
+  a.inv_d = 1.0f / (float)D;
   a.rope = rope;
   a.positions = positions;
   a.status = d_status;

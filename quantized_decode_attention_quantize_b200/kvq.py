@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -124,7 +125,7 @@ def lib():
             "kvq_decode_attention_paged": (I32, [FP, PP, P, P, I64, I32, P, I32, I32, ctypes.c_float, P,
                                                  I32, P, SZ, P, P]),
             "kvq_rope_table": (I32, [ctypes.POINTER(kvq_rope_spec), I64, I64, P, P]),
-            "kvq_norm_rope": (I32, [I32, I32, I64, ctypes.POINTER(kvq_head_rows), ctypes.POINTER(kvq_head_rows),
+            "kvq_norm_rope": (I32, [I32, I32, I64, P, P,
                                     ctypes.c_float, ctypes.c_float, ctypes.POINTER(kvq_rope), P, P, P]),
             "kvq_append_paged": (I32, [FP, PP, P, I64, I64, P, P, P, I64, I64, P, I64, I64,
                                        ctypes.POINTER(kvq_rope), P, P, P, P, P]),
@@ -397,6 +398,7 @@ class PagedCache:
             if self.block_table.dtype != torch.int32 or tuple(self.block_table.shape) != (num_seqs, max_blocks) or \
                     not self.block_table.is_contiguous():
                 raise ValueError("block_table must be a contiguous int32 [num_seqs][max_blocks]")
+        self.device = self.block_table.device
         self.struct = kvq_paged_cache(pool=self.pool.struct, num_seqs=num_seqs, max_blocks=max_blocks,
                                       block_table=self.block_table.data_ptr())
         for n, t in self.raw.items():
@@ -416,10 +418,6 @@ class PagedCache:
                 raise ValueError(f"{n}: a contiguous tensor of {need} bytes is needed")
             got[n] = t
         return got
-
-    @property
-    def device(self):
-        return self.block_table.device
 
     def array(self, name):
         return self.raw[name] if name in self.raw else self.pool.tensors[name]
@@ -461,44 +459,38 @@ def decode_attention_paged(fmt, cache: PagedCache, t_quant: torch.Tensor, t_res:
 
 
 # ---- serving steps around the paged cache ---------------------------------------------------
+# A decode step makes several of these calls, each of a few microseconds on the device: the checks
+# below avoid building messages and stream objects for calls that pass.
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_INT32 = torch.int32
+
+
 def _need(ok, what):
     if not ok:
         raise ValueError(what)
 
 
-class _On:
-    """The device of a call made current for its launch (and its stream for new tensors)."""
-
-    def __init__(self, device, stream):
-        _need(device.type == "cuda", "the tensors must be on a CUDA device")
-        _need(stream is None or stream.device == device, "the stream is on another device than the tensors")
-        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-        self.stream = None if stream is None else torch.cuda.stream(stream)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        if self.stream is not None:
-            self.stream.__enter__()
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *e):
-        if self.stream is not None:
-            self.stream.__exit__(*e)
-        if self.guard is not None:
-            self.guard.__exit__(*e)
+def _on(device, stream, body):
+    """body(raw stream) with `device` current, on `stream` or the device's current one (new
+    tensors belong to that stream)."""
+    if device.type != "cuda":
+        raise ValueError("the tensors must be on a CUDA device")
+    if stream is None and device.index == torch.cuda.current_device():
+        return body(_raw_stream(device.index))
+    _need(stream is None or stream.device == device, "the stream is on another device than the tensors")
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        return body(_raw_stream(device.index))
 
 
 def _ints(t, n, device, what):
-    _need(t.dtype == torch.int32 and t.dim() == 1 and t.numel() == n and t.is_contiguous() and t.device == device,
-          f"{what}: a contiguous int32 tensor of {n} values on the same device is needed")
-    return t.data_ptr()
+    if t.dtype is _INT32 and t.dim() == 1 and t.numel() == n and t.is_contiguous() and t.device == device:
+        return t.data_ptr()
+    raise ValueError(f"{what}: a contiguous int32 tensor of {n} values on the same device is needed")
 
 
 def _status_ptr(status, device):
-    if status is None:
-        return None
-    return _ints(status, 1, device, "status")
+    return None if status is None else _ints(status, 1, device, "status")
 
 
 def make_rope_spec(rot_dim: int, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, original_len=0.0, low=0.0, high=0.0,
@@ -518,11 +510,12 @@ def rope_table(spec: kvq_rope_spec, n_pos: int, pos0=0, out=None, device="cuda",
         device = torch.device(device)
         if device.type == "cuda" and device.index is None:
             device = torch.device("cuda", torch.cuda.current_device())
-    with _On(device, stream) as s:
-        if out is None:
-            out = torch.empty((n_pos, spec.rot_dim), dtype=torch.float32, device=device)
-        _check("kvq_rope_table", lib().kvq_rope_table(spec, pos0, n_pos, out.data_ptr(), s))
-    return out
+
+    def body(s):
+        t = torch.empty((n_pos, spec.rot_dim), dtype=torch.float32, device=device) if out is None else out
+        _check("kvq_rope_table", lib().kvq_rope_table(spec, pos0, n_pos, t.data_ptr(), s))
+        return t
+    return _on(device, stream, body)
 
 
 class Rope:
@@ -539,22 +532,27 @@ class Rope:
 def _rope_ptr(rope, device):
     if rope is None:
         return None
-    _need(rope.table.device == device, "the rotary table is on another device")
+    if rope.table.device != device:
+        raise ValueError("the rotary table is on another device")
     return rope.struct
 
 
+_HEAD_ROWS = struct.Struct("@PPqqqqiP")   # kvq_head_rows
+assert _HEAD_ROWS.size == ctypes.sizeof(kvq_head_rows)
+
+
 def _head_rows(x, y, weight, what):
-    _need(x.dim() == 3 and x.stride(2) == 1, f"{what}: [tokens, heads, head_dim] with contiguous channels is needed")
-    _need(y.shape == x.shape and y.dtype == x.dtype and y.device == x.device and y.stride(2) == 1,
-          f"{what}: the output's shape, dtype or device differs")
+    xt, xh, xc = x.stride()
+    yt, yh, yc = y.stride()
+    if xc != 1 or yc != 1 or y.shape != x.shape or y.dtype != x.dtype or y.device != x.device:
+        raise ValueError(f"{what}: channels must be contiguous, the output of the same shape, dtype and device")
+    w = 0
     if weight is not None:
-        _need(weight.dtype == x.dtype and weight.dim() == 1 and weight.numel() == x.shape[2] and
-              weight.is_contiguous() and weight.device == x.device,
-              f"{what}: a weight of [head_dim] in the rows' dtype is needed")
-    xt, xh, _ = x.stride()
-    yt, yh, _ = y.stride()
-    return kvq_head_rows(x.data_ptr(), y.data_ptr(), xt, xh, yt, yh, x.shape[1],
-                         None if weight is None else weight.data_ptr())
+        if weight.dtype != x.dtype or weight.dim() != 1 or weight.numel() != x.shape[2] or \
+                not weight.is_contiguous() or weight.device != x.device:
+            raise ValueError(f"{what}: a weight of [head_dim] in the rows' dtype is needed")
+        w = weight.data_ptr()
+    return _HEAD_ROWS.pack(x.data_ptr(), y.data_ptr(), xt, xh, yt, yh, x.shape[1], w)
 
 
 def norm_rope(q: torch.Tensor, k=None, q_weight=None, k_weight=None, eps=1e-6, weight_offset=0.0, rope=None,
@@ -562,24 +560,26 @@ def norm_rope(q: torch.Tensor, k=None, q_weight=None, k_weight=None, eps=1e-6, w
     """kvq_norm_rope: q [T, Hq, D] and k [T, Hk, D] (strided over tokens and heads) -> both
     normed per head (with a weight) and turned at `positions` (int32 [T]).  q_out = q and
     k_out = k work in place; new contiguous tensors otherwise."""
-    _need(q.dtype in KVQ_DTYPE and q.dim() == 3, "q: [tokens, heads, head_dim] in fp32, fp16 or bf16 is needed")
+    if q.dtype not in KVQ_DTYPE or q.dim() != 3:
+        raise ValueError("q: [tokens, heads, head_dim] in fp32, fp16 or bf16 is needed")
     T, _, D = q.shape
-    if k is not None:
-        _need(k.dim() == 3 and k.shape[0] == T and k.shape[2] == D and k.dtype == q.dtype and k.device == q.device,
-              "k: the tokens, head_dim, dtype and device of q are needed")
-    else:
+    d = q.device
+    if k is None:
         _need(k_weight is None and k_out is None, "k_weight and k_out go with k")
-    with _On(q.device, stream) as s:
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        rows_q = _head_rows(q, q_out, q_weight, "q")
-        rows_k = None if k is None else _head_rows(k, k_out, k_weight, "k")
-        pos = None if positions is None else _ints(positions, T, q.device, "positions")
-        _check("kvq_norm_rope", lib().kvq_norm_rope(D, KVQ_DTYPE[q.dtype], T, rows_q, rows_k, eps, weight_offset,
-                                                    _rope_ptr(rope, q.device), pos, _status_ptr(status, q.device), s))
-    return q_out, k_out
+    elif k.dim() != 3 or k.shape[0] != T or k.shape[2] != D or k.dtype != q.dtype or k.device != d:
+        raise ValueError("k: the tokens, head_dim, dtype and device of q are needed")
+
+    def body(s):
+        qo = torch.empty(q.shape, dtype=q.dtype, device=d) if q_out is None else q_out
+        ko, rows_k = None, None
+        if k is not None:
+            ko = torch.empty(k.shape, dtype=k.dtype, device=d) if k_out is None else k_out
+            rows_k = _head_rows(k, ko, k_weight, "k")
+        _check("kvq_norm_rope", lib().kvq_norm_rope(
+            D, KVQ_DTYPE[q.dtype], T, _head_rows(q, qo, q_weight, "q"), rows_k, eps, weight_offset, _rope_ptr(rope, d),
+            None if positions is None else _ints(positions, T, d, "positions"), _status_ptr(status, d), s))
+        return qo, ko
+    return _on(d, stream, body)
 
 
 def _batch(cache, cu, t_quant, t_res):
@@ -595,17 +595,21 @@ def append_paged(fmt, cache: PagedCache, cu_new: torch.Tensor, max_new: int, t_q
     t_quant_out / t_res_out."""
     dt, d = TORCH_DTYPE[fmt.src_dtype], cache.device
     rows = k_src.shape[0]
-    for x, what in ((k_src, "k_src"), (v_src, "v_src")):
-        _need(tuple(x.shape) == (rows, cache.H, fmt.head_dim) and x.dtype == dt and x.device == d and x.stride(2) == 1,
-              f"{what}: [rows, kv_heads, head_dim] in the format's source dtype is needed")
+    shape = (rows, cache.H, fmt.head_dim)
+    kt, kh, kc = k_src.stride() if k_src.dim() == 3 else (0, 0, 0)
+    vt, vh, vc = v_src.stride() if v_src.dim() == 3 else (0, 0, 0)
+    if k_src.shape != shape or v_src.shape != shape or k_src.dtype != dt or v_src.dtype != dt or kc != 1 or vc != 1 or \
+            k_src.device != d or v_src.device != d:
+        raise ValueError("k_src, v_src: [rows, kv_heads, head_dim] in the format's source dtype is needed")
     cu, tq, tr = _batch(cache, cu_new, t_quant, t_res)
     tq_o, tr_o = _ints(t_quant_out, cache.num_seqs, d, "t_quant_out"), _ints(t_res_out, cache.num_seqs, d, "t_res_out")
     pos = None if positions is None else _ints(positions, rows, d, "positions")
-    with _On(d, stream) as s:
+
+    def body(s):
         _check("kvq_append_paged", lib().kvq_append_paged(
-            fmt, cache.struct, cu, rows, max_new, tq, tr, k_src.data_ptr(), k_src.stride(0), k_src.stride(1),
-            v_src.data_ptr(), v_src.stride(0), v_src.stride(1), _rope_ptr(rope, d), pos, tq_o, tr_o,
-            _status_ptr(status, d), s))
+            fmt, cache.struct, cu, rows, max_new, tq, tr, k_src.data_ptr(), kt, kh, v_src.data_ptr(), vt, vh,
+            _rope_ptr(rope, d), pos, tq_o, tr_o, _status_ptr(status, d), s))
+    _on(d, stream, body)
 
 
 def read_paged(fmt, cache: PagedCache, cu: torch.Tensor, max_rows: int, first: torch.Tensor, t_quant: torch.Tensor,
@@ -618,17 +622,16 @@ def read_paged(fmt, cache: PagedCache, cu: torch.Tensor, max_rows: int, first: t
     cu, tq, tr = _batch(cache, cu, t_quant, t_res)
     p0 = _ints(first, cache.num_seqs, d, "first")
     for x in (k_out, v_out):
-        _need(x is None or (tuple(x.shape) == shape and x.dtype == dt and x.device == d and x.is_contiguous()),
-              "k_out / v_out: contiguous [n_rows, kv_heads, head_dim] in out_dtype is needed")
-    with _On(d, stream) as s:
-        if k_out is None:
-            k_out = torch.empty(shape, dtype=dt, device=d)
-        if v_out is None:
-            v_out = torch.empty(shape, dtype=dt, device=d)
-        _check("kvq_read_paged", lib().kvq_read_paged(fmt, cache.struct, cu, n_rows, max_rows, p0, tq, tr,
-                                                      k_out.data_ptr(), v_out.data_ptr(), out_dtype,
-                                                      _status_ptr(status, d), s))
-    return k_out, v_out
+        if x is not None and (x.shape != shape or x.dtype != dt or x.device != d or not x.is_contiguous()):
+            raise ValueError("k_out / v_out: contiguous [n_rows, kv_heads, head_dim] in out_dtype is needed")
+
+    def body(s):
+        k = torch.empty(shape, dtype=dt, device=d) if k_out is None else k_out
+        v = torch.empty(shape, dtype=dt, device=d) if v_out is None else v_out
+        _check("kvq_read_paged", lib().kvq_read_paged(fmt, cache.struct, cu, n_rows, max_rows, p0, tq, tr, k.data_ptr(),
+                                                      v.data_ptr(), out_dtype, _status_ptr(status, d), s))
+        return k, v
+    return _on(d, stream, body)
 
 
 def attention_paged_workspace_bytes(fmt, num_seqs, Hq, Hkv, n_rows, max_new, max_t_quant, max_t_res) -> int:
@@ -641,25 +644,29 @@ def attention_paged(fmt, cache: PagedCache, cu_q: torch.Tensor, max_new: int, t_
     """kvq_attention_paged: q [rows, Hq, D] contiguous, the last cu_q[s + 1] - cu_q[s] tokens of
     every sequence -> out [rows, Hq, D] (out_dtype: q's by default); lse: fp32 [rows, Hq]."""
     d = cache.device
-    _need(q.dtype in KVQ_DTYPE and q.dim() == 3 and q.shape[2] == fmt.head_dim and q.is_contiguous() and q.device == d,
-          "q: a contiguous [rows, q_heads, head_dim] in fp32, fp16 or bf16 is needed")
+    if q.dtype not in KVQ_DTYPE or q.dim() != 3 or q.shape[2] != fmt.head_dim or not q.is_contiguous() or q.device != d:
+        raise ValueError("q: a contiguous [rows, q_heads, head_dim] in fp32, fp16 or bf16 is needed")
     rows, Hq, _ = q.shape
     out_dtype = KVQ_DTYPE[q.dtype] if out_dtype is None else out_dtype
-    _need(out is None or (out.shape == q.shape and out.dtype == TORCH_DTYPE[out_dtype] and out.device == d and
-                          out.is_contiguous()), "out: a contiguous tensor of q's shape in out_dtype is needed")
-    _need(lse is None or (tuple(lse.shape) == (rows, Hq) and lse.dtype == torch.float32 and lse.device == d and
-                          lse.is_contiguous()), "lse: a contiguous fp32 [rows, q_heads] tensor is needed")
+    dt = TORCH_DTYPE[out_dtype]
+    if out is not None and (out.shape != q.shape or out.dtype != dt or out.device != d or not out.is_contiguous()):
+        raise ValueError("out: a contiguous tensor of q's shape in out_dtype is needed")
+    if lse is not None and (lse.shape != (rows, Hq) or lse.dtype != torch.float32 or lse.device != d or
+                            not lse.is_contiguous()):
+        raise ValueError("lse: a contiguous fp32 [rows, q_heads] tensor is needed")
+    if workspace is not None and (not workspace.is_contiguous() or workspace.device != d):
+        raise ValueError("workspace: a contiguous tensor on q's device")
     cu, tq, tr = _batch(cache, cu_q, t_quant, t_res)
-    with _On(d, stream) as s:
-        if out is None:
-            out = torch.empty(q.shape, dtype=TORCH_DTYPE[out_dtype], device=d)
-        if workspace is None:
-            need = attention_paged_workspace_bytes(fmt, cache.num_seqs, Hq, cache.H, rows, max_new, max_t_quant,
-                                                   max_t_res)
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=d)
-        _need(workspace.is_contiguous() and workspace.device == d, "workspace: a contiguous tensor on q's device")
+
+    def body(s):
+        o = torch.empty(q.shape, dtype=dt, device=d) if out is None else out
+        w = workspace
+        if w is None:
+            need = attention_paged_workspace_bytes(fmt, cache.num_seqs, Hq, cache.H, rows, max_new, max_t_quant, max_t_res)
+            w = torch.empty(max(need, 16), dtype=torch.uint8, device=d)
         _check("kvq_attention_paged", lib().kvq_attention_paged(
             fmt, cache.struct, cu, rows, max_new, tq, tr, max_t_quant, max_t_res, q.data_ptr(), KVQ_DTYPE[q.dtype],
-            Hq, scale, int(causal), out.data_ptr(), out_dtype, None if lse is None else lse.data_ptr(),
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), _status_ptr(status, d), s))
-    return out
+            Hq, scale, int(causal), o.data_ptr(), out_dtype, None if lse is None else lse.data_ptr(), w.data_ptr(),
+            w.numel() * w.element_size(), _status_ptr(status, d), s))
+        return o
+    return _on(d, stream, body)

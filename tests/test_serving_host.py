@@ -60,6 +60,7 @@ def test_norm_rope_refuses():
         return kvq.kvq_rope(**dict(dict(table=0x300000, n_pos=8, rot_dim=64, interleaved=0), **kw))
 
     def call(D=128, dt=kvq.BF16, n=4, q=rows(), k=None, eps=1e-6, off=0.0, r=None, pos=None, st=None):
+        q, k = (None if x is None else ctypes.byref(x) for x in (q, k))
         return kvq.lib().kvq_norm_rope(D, dt, n, q, k, eps, off, r, pos, st, None)
 
     for kw in (dict(D=120), dict(D=0), dict(D=272), dict(dt=5), dict(n=-1), dict(q=None), dict(q=rows(heads=0)),
