@@ -187,6 +187,7 @@ struct ReadArgs {
   Layout L;
   PagedBatch b;
   const int32_t* first;
+  int direct;               // four CTAs per sequence (set by the launcher)
   void* out[2];
   int out_dtype;
   const void* sink[2];
