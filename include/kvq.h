@@ -473,7 +473,9 @@ kvq_status kvq_decode_attention_paged(const kvq_format* fmt, const kvq_paged_cac
  * Ragged batches.  A batch of num_seqs sequences is given as rows back to back, the rows
  * of sequence s being [cu[s], cu[s + 1]) of the row arrays: cu is device int32
  * [num_seqs + 1], ascending, cu[0] >= 0 and cu[num_seqs] <= n_rows, the rows the arrays
- * hold.  Rows outside every sequence are left alone.  An empty sequence is allowed.
+ * hold.  Rows outside every sequence are left alone.  An empty sequence is allowed.  Where
+ * cu does not ascend KVQ_DEV_BOUNDS is raised and nothing is promised for the batch's
+ * other sequences but that no memory outside the arrays is touched.
  *
  * Lengths.  A sequence holds n_sink + t_quant[s] + t_res[s] tokens in position order:
  * its sink rows, packed tokens [0, t_quant[s]) and window rows [0, t_res[s]).  While the
@@ -588,7 +590,10 @@ kvq_status kvq_read_paged(const kvq_format* fmt, const kvq_paged_cache* cache, c
                           int32_t* d_status, void* stream);
 
 /* Workspace bytes for kvq_attention_paged with these sizes (depends on the current
- * device's SM count); 0 for sizes it refuses. */
+ * device's SM count); 0 for sizes it refuses.  For long chunks (more than 256 query rows
+ * per KV head and sequence on average) it includes room for the pages expanded to fp16, 64 KB per
+ * page of each sequence's bound and KV head, where that is at most 4 GiB; a smaller
+ * workspace, down to what the call needs for other sizes, runs too, more slowly. */
 size_t kvq_attention_paged_workspace_bytes(const kvq_format* fmt, int32_t num_seqs, int32_t q_heads,
                                            int32_t kv_heads, int64_t n_rows, int64_t max_new,
                                            int64_t max_t_quant, int32_t max_t_res);
@@ -604,13 +609,19 @@ size_t kvq_attention_paged_workspace_bytes(const kvq_format* fmt, int32_t num_se
  * that sees no token (n > L) gets out = 0 and lse = -inf.  The products run on the tensor
  * cores with fp16 operands and fp32 sums: queries (scaled by a power of two of their own
  * row), probabilities and reconstructed or raw keys and values are each rounded to fp16
- * once.  A raw key or value beyond fp16's range raises KVQ_DEV_RANGE, a NaN or Inf one
- * KVQ_DEV_NONFINITE; either counts as 0 there, so rows that do not see it are unaffected.
+ * once (for a few rows: query times key scale, and probability times value scale).  A raw
+ * key or value beyond fp16's range raises KVQ_DEV_RANGE, a NaN or Inf one
+ * KVQ_DEV_NONFINITE; either counts as 0 there, as do packed values whose scale or
+ * zero-point did not fit fp16 at their append, so rows that do not see them are unaffected.
+ * The work is cut by the lengths of the whole batch, and where it is cut sums are rounded
+ * otherwise: the same batch gives the same bits, another batch the same values only within
+ * those roundings.
  * max_new, max_t_quant, max_t_res: host bounds as in the calls above.  A sequence whose
  * numbers are out of range (t_quant above max_t_quant and the like) keeps its rows as they
  * were and raises KVQ_DEV_BOUNDS; a page missing from the table or outside the pool raises
  * it too and its tokens are read from block 0.  Formats: those of the paged cache above
- * (D = 128, group_tokens 128), q_heads / kv_heads <= 16. */
+ * (D = 128, group_tokens 128), q_heads / kv_heads <= 16; n_rows * q_heads < 2^31 and
+ * max_t_quant < 2^30. */
 kvq_status kvq_attention_paged(const kvq_format* fmt, const kvq_paged_cache* cache, const int32_t* cu_q,
                                int64_t n_rows, int64_t max_new, const int32_t* t_quant,
                                const int32_t* t_res, int64_t max_t_quant, int32_t max_t_res,

@@ -448,10 +448,12 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_narrow_kernel(const __gri
             int left[4];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const bool there = 16 * k0 + g + 8 * e < valid;   // behind the end anything may lie
-              s[e] = there ? __half2float(vs[8 * e]) : 1.0f;
-              z[e] = there ? __half2float(vs[128 + 8 * e]) : 0.0f;
-              asm("lg2.approx.f32 %0, %1;" : "=f"(ls[e]) : "f"(s[e]));
+              // behind the end anything may lie; what did not fit fp16 when it was packed counts as zero
+              s[e] = __half2float(vs[8 * e]);
+              z[e] = __half2float(vs[128 + 8 * e]);
+              const bool there = 16 * k0 + g + 8 * e < valid && s[e] <= 65504.0f && fabsf(z[e]) <= 65504.0f;
+              if (!there) s[e] = z[e] = 0.0f;
+              asm("lg2.approx.f32 %0, %1;" : "=f"(ls[e]) : "f"(there ? s[e] : 1.0f));
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q) left[q] = cols[q] - 16 * k0;

@@ -267,8 +267,14 @@ __device__ __forceinline__ void put_keys(const void* codes, const void* scale, c
          code2<0x000F000Fu, 0x64006400u>(y, s2, z2), code2<0x00F000F0u, 0x54005400u>(y, s3, z3));
   }
 }
+// All ones in the halves of x that hold finite numbers.
+__device__ __forceinline__ uint32_t finite2(uint32_t x) {
+  const __half2 h = __habs2(*reinterpret_cast<const __half2*>(&x));
+  return __hle2_mask(h, __half2half2(__ushort_as_half(0x7BFF)));
+}
 // A packed group's values: thread t takes word W = t % 16 (eight channels) of the token octets t / 16 and
-// t / 16 + 8.  Tokens past the group's end count as zero, whatever lies there.
+// t / 16 + 8.  Tokens past the group's end count as zero, whatever lies there, and so do tokens whose scale or
+// zero-point did not fit fp16 when they were packed: a weight of 0 would not silence them.
 __device__ __forceinline__ void put_values(const void* codes, const void* scale, const void* zero, uint32_t slot, int t,
                                            int valid) {
   const int W = t & 15;
@@ -282,7 +288,7 @@ __device__ __forceinline__ void put_values(const void* codes, const void* scale,
     for (int j = 0; j < 4; ++j) {
       w[j] = c[16 * j];
       const int left = valid - 8 * o - 2 * j;
-      const uint32_t m = left >= 2 ? 0xffffffffu : left == 1 ? 0x0000ffffu : 0u;
+      const uint32_t m = (left >= 2 ? 0xffffffffu : left == 1 ? 0x0000ffffu : 0u) & finite2(s[j]) & finite2(z[j]);
       s[j] &= m;
       z[j] &= m;
     }

@@ -444,6 +444,28 @@ def test_attention_rows_without_tokens_and_steep_scores():
     p.check_attention(q, scale, out, lse, counts, True, F32)
 
 
+@pytest.mark.parametrize("counts", [[2, 1, 3], [40, 100, 1], [300, 130, 70]])
+def test_attention_over_nothing(counts):
+    # sequences without a single token, without a sink, at each of the kernels
+    p = Paged(fmt(n_sink=0), 2, 3, 2, seed=64)
+    p.fill([0, 130, 0])
+    q, scale, out, lse = p.attend(counts, 4)
+    assert int(p.status) == 0
+    p.check_attention(q, scale, out, lse, counts, True, F32)
+
+
+@pytest.mark.parametrize("n", [4, 30, 200])
+def test_attention_ignores_unseen_values_that_did_not_fit(n):
+    # a packed value token with an infinite scale, later than the queries' first rows see
+    p = Paged(fmt(n_sink=0), 2, 1, 3, seed=65)
+    p.fill([256])
+    q, scale, clean, _ = p.attend([n], 4)
+    for name in ("v_scale", "v_zero"):
+        p.gpu.pool.tensors[name].view(torch.float16).view(-1, 2, 128)[int(p.table[0, 1]), :, 126] = float("inf")
+    _, _, out, _ = p.attend([n], 4, q=q)
+    assert torch.equal(out[:n - 2], clean[:n - 2])
+
+
 def test_attention_agrees_with_decode():
     p = Paged(fmt(), 2, 4, 8, seed=43)
     p.fill([700, 129, 1, 330])
