@@ -180,7 +180,7 @@ __device__ __forceinline__ void turn_rows(const AppendArgs& a, int which, int o,
 // 30k tokens of 8 heads in bf16, 310 us with one CTA, 129 with two, 116 with three (1.2 TB/s of rows in and
 // codes out; bound by the chain of dependent loads and barriers of a unit, and by its arithmetic).
 template <int DT, bool ROT>
-__global__ void __launch_bounds__(kThreads, DT == KVQ_F32 || ROT ? 1 : 2)
+__global__ void __launch_bounds__(kThreads, DT == KVQ_F32 || ROT ? 1 : 3)
     append_paged_kernel(const __grid_constant__ AppendArgs a) {
   __shared__ float pmin[8][128], pmax[8][128];
   __shared__ float sf[128], zf[128], rf[128];
