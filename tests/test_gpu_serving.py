@@ -639,3 +639,40 @@ def test_attention_repeats_itself_bit_for_bit():
     for _ in range(3):
         _, _, again, lse2 = p.attend(counts, 4, q=q)
         assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+def test_pools_past_32_bits_of_offset():
+    # 40 000 blocks of 8 heads: 2.6 GB of key codes; the sequences' blocks lie anywhere among them
+    p = Paged(fmt(), 8, 2, 5, seed=70, spare=40000)
+    assert p.gpu.pool.tensors["k_codes"].numel() > 2 ** 31 and p.table.max() > 33000
+    p.append([500, 300], rope_of())
+    for counts in ([2, 1], [150, 40], [500, 300]):
+        q, scale, out, lse = p.attend(counts, 2)
+        assert int(p.status) == 0
+        for s in range(2):
+            ref, _ = serving.attention(p.ora, s, p.tq[s], p.tr[s],
+                                       q[cu_of(counts)[s + 1] - 1:cu_of(counts)[s + 1]].astype(np.float64), scale)
+            got = np64(out[cu_of(counts)[s + 1] - 1])
+            # 2e-3: twice the relative L2 bar of the decode's own tests for fp32 output
+            assert np.linalg.norm(got - ref[0]) <= 2e-3 * np.linalg.norm(ref)
+    k, v = kvq.read_paged(p.fmt, p.gpu, ints([0, 500, 800]), 500, ints([0, 0]), ints(p.tq), ints(p.tr), 800)
+    for s, (lo, hi) in enumerate(((0, 500), (500, 800))):
+        K, V = serving.tokens(p.ora, s, p.tq[s], p.tr[s])
+        np.testing.assert_array_equal(np64(k[lo:hi]), serving.round_src(K.swapaxes(0, 1), BF16))
+        np.testing.assert_array_equal(np64(v[lo:hi]), serving.round_src(V.swapaxes(0, 1), BF16))
+
+
+def test_many_sequences():
+    # 700 sequences: the partition, the searches and the flat grids over more than one pass of a warp
+    S = 700
+    p = Paged(fmt(), 1, S, 2, seed=71)
+    rng = np.random.default_rng(72)
+    lengths = rng.integers(0, 230, S)
+    lengths[rng.integers(0, S, 150)] = 0
+    p.append([int(x) for x in lengths], rope_of(32, True))
+    p.check()
+    for most in (3, 70):
+        counts = [int(min(x, c)) for x, c in zip(lengths, rng.integers(0, most + 1, S))]
+        q, scale, out, lse = p.attend(counts, 2, out_dt=BF16)
+        assert int(p.status) == 0
+        p.check_attention(q, scale, out, lse, counts, True, BF16, seqs=list(range(0, S, 9)) + [S - 1])
