@@ -542,7 +542,8 @@ typedef struct kvq_head_rows {
  * every row x of head_dim channels (a multiple of 16 in [16, 256]; fp32, fp16 or bf16)
  *   u = x / sqrt(mean(x^2) + eps) * (weight_offset + weight)      (u = x without a weight)
  *   y = u turned by the table's row of the token's position
- * in fp32, rounded once to `dtype`.  `k` may be NULL (queries only).  rope may be NULL (norm
+ * in fp32, rounded once to `dtype`; squares beyond fp32's range do not matter.  A NaN or
+ * Inf raises KVQ_DEV_NONFINITE.  `k` may be NULL (queries only).  rope may be NULL (norm
  * only).  positions: device int32 [n_tokens], NULL for position = token index; a position
  * outside [0, n_pos) leaves the row unturned and raises KVQ_DEV_BOUNDS. */
 kvq_status kvq_norm_rope(int32_t head_dim, int32_t dtype, int64_t n_tokens, const kvq_head_rows* q,

@@ -117,6 +117,7 @@ kvq_status kvq_rope_table(const kvq_rope_spec* p, int64_t pos0, int64_t n_pos, f
         break;
       default: f[i] = w;
     }
+    if (!std::isfinite(f[i])) return KVQ_ERR_INVALID;   // a base or factor beyond what double carries
   }
   return launched(launch_rope_table(f, half, p->amplitude, pos0, n_pos, table, reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -11,7 +11,8 @@ namespace {
 // Row p: a cos(p f_i), i < R/2, then a sin(p f_i), in double, rounded once to fp32.  A thread takes one pair
 // over kSteps consecutive positions: the first angle and the step by sincos, the others by turning
 // (four fused operations), which adds at most kSteps 2^-52 to the 2^-25 of the rounding.  Bound by the
-// stores (4 R bytes a position).  131072 positions of 128: 71.8 us with a sincos for each entry.
+// stores (4 R bytes a position).  131072 positions of 128: 15.3 us (4.4 TB/s stored), 71.8 with a sincos for each
+// entry.
 struct TableArgs {
   double freq[128];
   int half;
@@ -45,7 +46,8 @@ __global__ void __launch_bounds__(256) rope_table_kernel(const __grid_constant__
 
 // ---- norm and rotation -----------------------------------------------------------------
 // LPR lanes (8, 16 or 32) hold one head row, an octet each; the mean square meets over them
-// by shuffles, and the half-layout partner octet comes from its lane.
+// by shuffles, and the half-layout partner octet comes from its lane.  Bound by the rows read and written and
+// the waits on those loads; two heads to a group and four CTAs per SM keep enough of them in flight.
 struct NormArgs {
   HeadRows side[2];
   int D, dtype;
@@ -111,16 +113,30 @@ __global__ void __launch_bounds__(256, 4) norm_rope_kernel(const __grid_constant
 #pragma unroll
       for (int j = 0; j < 8; ++j) bad |= !isfinite(x[k][j]);
     }
-    if (S.weight) {   // alike over the lanes of a row; rows of one warp may differ
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[k][j] *= w[j];
-    }
 #pragma unroll
     for (int m = 1; m < LPR; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-    if (S.weight) {
-      const float r = rsqrtf(fmaf(ss, a.inv_d, a.eps));
+    if (S.weight) {   // alike over the lanes of a row; rows of one warp may differ
+      float eps = a.eps, r = fmaf(ss, a.inv_d, eps);
+      // Squares outside fp32's range: the row is taken 2^70 times smaller or larger, eps by the square of it.
+      const bool big = !(ss <= 0x1p126f), small = r < 0x1p-90f;
+      if (big || small) {
+        const float by = big ? 0x1p-70f : 0x1p70f;
+        eps *= by;
+        eps *= by;
+        ss = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[k][j] *= r;
+        for (int j = 0; j < 8; ++j) {
+          x[k][j] *= by;
+          ss = fmaf(x[k][j], x[k][j], ss);
+        }
+        const unsigned row = LPR == 32 ? 0xffffffffu : ((1u << (LPR & 31)) - 1u) << (threadIdx.x & 31 & ~(LPR - 1));
+#pragma unroll
+        for (int m = 1; m < LPR; m <<= 1) ss += __shfl_xor_sync(row, ss, m);
+        r = fmaf(ss, a.inv_d, eps);
+      }
+      r = rsqrtf(r);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[k][j] = x[k][j] * w[j] * r;
     }
     if (a.rope.table) {
       float p[8];

@@ -159,6 +159,21 @@ def test_norm_rope_flags_positions_and_values():
     assert kvq.norm_rope(z[:0], q_weight=w)[0].shape == (0, 1, 64)
 
 
+@pytest.mark.parametrize("D", [48, 128, 256])
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("eps", [0.0, 1e-30, 1e-6])
+def test_norm_of_rows_whose_squares_leave_fp32(D, dt, eps):
+    rng = np.random.default_rng(D + dt)
+    x = normal(rng, (6, 4, D), dt)
+    x *= np.exp2(np.array([100, -80, 0, 64, -64, 120], np.float32))[:, None, None]   # within one warp, too
+    x[:, 1] *= np.float32(2.0 ** -20)
+    w = normal(rng, (D,), dt)
+    st = status0()
+    q, _ = kvq.norm_rope(dev(x, dt), q_weight=dev(w, dt), eps=eps, status=st)
+    check_norm(q, x, w, np.float64(np.float32(eps)), 0.0, None, False, dt)
+    assert int(st) == 0
+
+
 # ---- cache pairs -------------------------------------------------------------------------------
 class Paged:
     """The library's and the oracle's paged cache side by side."""

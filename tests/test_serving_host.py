@@ -31,7 +31,7 @@ def cache(f, H=2, S=3, blocks=4, cols=2):
 @fake_pointers
 @pytest.mark.parametrize("kw,pos0,n", [
     (dict(rot_dim=24), 0, 4), (dict(rot_dim=0), 0, 4), (dict(rot_dim=272), 0, 4), (dict(base=1.0), 0, 4),
-    (dict(base=float("nan")), 0, 4), (dict(scaling=4), 0, 4), (dict(scaling=1, factor=0.0), 0, 4),
+    (dict(base=float("nan")), 0, 4), (dict(scaling=4), 0, 4), (dict(scaling=1, factor=0.0), 0, 4), (dict(scaling=1, factor=1e-310), 0, 4),
     (dict(scaling=2, factor=2.0), 0, 4), (dict(scaling=2, factor=2.0, original_len=8.0, low=4.0, high=1.0), 0, 4),
     (dict(amplitude=0.0), 0, 4), (dict(amplitude=float("inf")), 0, 4), (dict(), -1, 4), (dict(), 0, -1),
     (dict(), 2 ** 31 - 1, 2)])
