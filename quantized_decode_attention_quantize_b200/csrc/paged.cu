@@ -446,7 +446,7 @@ __device__ __forceinline__ ReadSeq read_seq(const ReadArgs& a, int s) {
 }
 
 // Grid (units, kv head x {keys, values}); thread (r, o): octet o of rows r + 16 j (keys) or pairs r + 16 j
-// (values).  Bound by the rows written.
+// (values).  Bound by the rows written; four CTAs per SM cover the dependent loads (table, page, codes).
 template <int OD>
 __global__ void __launch_bounds__(kThreads, 4) read_paged_kernel(const __grid_constant__ ReadArgs a) {
   griddep_wait();

@@ -81,12 +81,4 @@ __device__ __forceinline__ void store8(void* base, int64_t i, int dtype, const f
   }
 }
 
-// Values rounded to `dtype` and back.
-__device__ __forceinline__ void round8(float (&x)[8], int dtype) {
-  if (dtype == KVQ_F32) return;
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    x[j] = dtype == KVQ_F16 ? __half2float(__float2half_rn(x[j])) : __bfloat162float(__float2bfloat16_rn(x[j]));
-}
-
 }  // namespace kvq
