@@ -15,7 +15,7 @@
 // row: with key scales up to 65504 / 15 the products stay below 65504.
 //
 // What bounds it: the expansion and the softmax on CUDA cores (about 200 instructions per 16 tokens and warp);
-// the packed bytes pass once per 16 rows.  4 tokens x 8 sequences over 32768 and fewer, 8 x 4 heads: 98 us, of
+// the packed bytes pass once per 16 rows.  4 tokens x 8 sequences over 32768 and fewer, 8 x 4 heads: 99 us, of
 // which the tiles take 67 (1250 cycles per 16 tokens and warp, two warps per scheduler at 0.3 instructions a clock).
 #include "attn_paged.cuh"
 

@@ -479,8 +479,8 @@ cudaError_t launch_merge(const AttnArgs& a, const Work& w, int runs, cudaStream_
 bool attn_wide_pays(int num_seqs, int G, int64_t n_rows) { return n_rows * G > (int64_t)num_seqs * 256; }
 
 // Blocks of 16 rows, a warp each, up to 64 rows a sequence; blocks of 256 on the whole CTA above.  16 rows (4 tokens
-// x 4 heads) of 8 sequences over 32768 and fewer: 98 us against 225 on the whole CTA; at 64 rows the pages pass four
-// times and the two are about even.
+// x 4 heads) of 8 sequences over 32768 and fewer: 99 us against 225 on the whole CTA; 64 rows 199 (the pages pass
+// four times), 68 to 96 rows on the whole CTA 211 to 222.
 constexpr int kNarrowRows = 64, kNarrowWarps = 8;
 bool narrow(int G, int64_t max_new) { return max_new * G <= kNarrowRows; }
 size_t make_work_for(int G, int64_t max_new, void* ws, Work* w, int* runs) {

@@ -328,8 +328,8 @@ __device__ __forceinline__ void softmax_warp(const AttnArgs& a, const Work& work
 }
 
 // 2.2 us per pair of a 256-row block and a 128-token tile, of which products and copies alone take 1.86 (64 KB
-// per pair from L2 are 10 TB/s over all SMs); 2048 tokens x 8 x 4 heads over 16384: 680 us with the expansion,
-// 859 TFLOP/s.
+// per pair from L2 are 10 TB/s over all SMs); 2048 tokens x 8 x 4 heads over 16384: 683 us with the expansion,
+// 855 TFLOP/s.
 __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_constant__ AttnArgs a,
                                                                 const __grid_constant__ Work work, const char* tiles,
                                                                 int64_t bound) {
