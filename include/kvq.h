@@ -610,10 +610,15 @@ size_t kvq_attention_paged_workspace_bytes(const kvq_format* fmt, int32_t num_se
  * that sees no token (n > L) gets out = 0 and lse = -inf.  The products run on the tensor
  * cores with fp16 operands and fp32 sums: queries (scaled by a power of two of their own
  * row), probabilities and reconstructed or raw keys and values are each rounded to fp16
- * once (for a few rows: query times key scale, and probability times value scale).  A raw
- * key or value beyond fp16's range raises KVQ_DEV_RANGE, a NaN or Inf one
- * KVQ_DEV_NONFINITE; either counts as 0 there, as do packed values whose scale or
- * zero-point did not fit fp16 at their append, so rows that do not see them are unaffected.
+ * once (for a few rows: query times key scale, and probability times value scale).  Keys
+ * and values that fp16 does not hold, in the tokens that a block of rows reads: a NaN or Inf
+ * raw one raises KVQ_DEV_NONFINITE and counts as 0; a raw one beyond +-65504 raises
+ * KVQ_DEV_RANGE and counts as 0; packed ones whose scale or zero-point did not fit fp16 at
+ * their append raise KVQ_DEV_RANGE and count as 0 (a key channel of its group, a value
+ * token); packed ones of a fitting scale and zero-point whose largest code gives more than
+ * 65504 raise KVQ_DEV_RANGE, and numbers beyond it count as 65504 (for a few rows, at most
+ * 64 per KV head with max_new: as they are).  Rows that do not see such a token are
+ * unaffected, save by a key channel that did not fit, which its whole group shares.
  * The work is cut by the lengths of the whole batch, and where it is cut sums are rounded
  * otherwise: the same batch gives the same bits, another batch the same values only within
  * those roundings.

@@ -159,6 +159,26 @@ __device__ __forceinline__ void value_tile(State& st, int c, const uint32_t (&w)
   mma16816(st.o[c][1], a0, a1, a2, a3, b[1][0], b[1][1]);
 }
 
+// A group's metadata, four channels and four tokens a lane: what gives numbers beyond fp16 is flagged, and key
+// channels with an infinity or NaN are set to zero where they lie (value tokens are as they are read).
+__device__ __forceinline__ void check_group(uint8_t* in, int lane, int valid, int& flags) {
+  uint2* ks = reinterpret_cast<uint2*>(in + kKMeta) + lane;
+  uint2* kz = reinterpret_cast<uint2*>(in + kKMeta + 256) + lane;
+  const uint2 vs = reinterpret_cast<const uint2*>(in + kVMeta)[lane], vz = reinterpret_cast<const uint2*>(in + kVMeta + 256)[lane];
+  const uint2 s = *ks, z = *kz;
+  const int left = valid - 4 * lane;
+  const uint32_t k = finite2(h2fma(kFifteen2, s.x, z.x)) & finite2(h2fma(kFifteen2, s.y, z.y));
+  const uint32_t v = (finite2(h2fma(kThree2, vs.x, vz.x)) | (left >= 2 ? 0u : left == 1 ? 0xffff0000u : 0xffffffffu)) &
+                     (finite2(h2fma(kThree2, vs.y, vz.y)) | (left >= 4 ? 0u : left == 3 ? 0xffff0000u : 0xffffffffu));
+  if (!__any_sync(0xffffffffu, (k & v) != 0xffffffffu)) return;
+  if ((k & v) != 0xffffffffu) flags |= KVQ_DEV_RANGE;
+  const uint32_t mx = finite2(s.x) & finite2(z.x), my = finite2(s.y) & finite2(z.y);
+  *ks = make_uint2(s.x & mx, s.y & my);
+  *kz = make_uint2(z.x & mx, z.y & my);
+  fence_async_smem();   // before the next group's copies into this stage
+  __syncwarp();
+}
+
 __global__ void __launch_bounds__(32 * kWarps, 1) attn_narrow_kernel(const __grid_constant__ AttnArgs a,
                                                                      const __grid_constant__ Work work) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -372,7 +392,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_narrow_kernel(const __gri
             break;
           }
           ++taken;
-          const uint8_t* in = stages + slot * kStage;
+          uint8_t* in = stages + slot * kStage;
+          const int valid = min(128, c.tq - 128 * gi);
+          check_group(in, lane, valid, flags);
           // this group's B fragments and zero-point sums
           uint32_t bs[2][16];
           float mul[4], add[4], zd[2] = {0.0f, 0.0f};
@@ -405,7 +427,6 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_narrow_kernel(const __gri
           }
           int cols[4];
           bool edge = false;
-          const int valid = min(128, c.tq - 128 * gi);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             add[q] = cs[q] * __shfl_sync(0xffffffffu, zd[q >> 1], 4 * (2 * t + (q & 1)));

@@ -96,8 +96,8 @@ __device__ __forceinline__ void producer(const AttnArgs& a, Small* sm, uint32_t 
         ++groups;
         if (!(ok = mbar_wait(smem_u32(VALUES ? &sm->v_in[st] : &sm->k_in[st]), round, &sm->stop))) break;
         const uint8_t* in = stages + st * (kStageK + kStageV) + (VALUES ? kStageK : 0);
-        if (VALUES) put_values(in, in + 4096, in + 4352, dst, t, min(128, c.tq - 128 * (at - c.n_raw)));
-        else put_keys(in, in + 8192, in + 8448, dst, t);
+        if (VALUES) flags |= put_values(in, in + 4096, in + 4352, dst, t, min(128, c.tq - 128 * (at - c.n_raw)));
+        else flags |= put_keys(in, in + 8192, in + 8448, dst, t);
         fence_async_smem();
         mbar_arrive(smem_u32(&sm->full[slot]));
         __syncwarp();

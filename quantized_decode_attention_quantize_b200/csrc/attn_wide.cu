@@ -88,8 +88,8 @@ __global__ void __launch_bounds__(kExpandThreads, 3) expand_kernel(const __grid_
       const char* codes = reinterpret_cast<const char*>(S.codes) + slab * S.code_slab_bytes;
       const char* scale = reinterpret_cast<const char*>(S.scale) + slab * 256;
       const char* zero = reinterpret_cast<const char*>(S.zero) + slab * 256;
-      if (threadIdx.x < 128) put_keys(codes, scale, zero, dst, t);
-      else put_values(codes, scale, zero, dst, t, min(128, q.tq - 128 * g));
+      if (threadIdx.x < 128) flags |= put_keys(codes, scale, zero, dst, t);
+      else flags |= put_values(codes, scale, zero, dst, t, min(128, q.tq - 128 * g));
     }
     fence_async_smem();
     __syncthreads();

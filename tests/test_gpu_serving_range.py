@@ -1,0 +1,106 @@
+"""The serving steps at the ends of their number ranges: packed and raw magnitudes beyond fp16,
+scales near its end, rows that are not finite, and what the status word says of them.
+
+Bars as in test_gpu_serving, u = 2^-11 being half a step of fp16, with one term more.  Attention of at
+most 64 query rows per KV head and sequence sums p s c in fp16 products and p z apart, so the rounding of
+p s counts against s c = v - z and not against v: the sums of p |v| become sums of p (|v| + |z|), z the token's
+zero-point.  Its key products round q s against c - 8, at most 8 s = (k_15 - k_0) 8 / 15 per channel, k_0 and k_15
+the ends of the channel's range: below the largest |q| |k| of the group's tokens where the ends are reached."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import synth
+from oracle import serving
+from oracle.formats import BF16, F16, F32
+from quantized_decode_attention_quantize_b200 import kvq
+from tests.gpu_util import dev
+from tests.test_gpu_serving import POOL, U, WHT, Paged, check_norm, cu_of, fmt, ints, normal, np64, rope_of, status0
+
+pytestmark = pytest.mark.gpu
+RANGE, NONFINITE, BOUNDS = kvq.KVQ_DEV_RANGE, kvq.KVQ_DEV_NONFINITE, kvq.KVQ_DEV_BOUNDS
+TOP = 65504.0
+
+
+def filled(fd, k, v, H=2, blocks=5):
+    """One sequence without a sink that holds the rows k, v [L, H, 128] (exact in the source type)."""
+    p = Paged(fd, H, 1, blocks, seed=3)
+    out = ints([0]), ints([0])
+    kvq.append_paged(p.fmt, p.gpu, ints([0, len(k)]), len(k), ints([0]), ints([0]), dev(k, p.dt), dev(v, p.dt), *out,
+                     status=p.status)
+    tq, tr = serving.append(p.ora, 0, 0, 0, k.astype(np.float64), v.astype(np.float64))
+    p.tq, p.tr = [tq], [tr]
+    assert out[0].tolist() == p.tq and out[1].tolist() == p.tr
+    return p
+
+
+def check_rows(p, q, scale, out, lse, K, V):
+    """Causal rows of the one sequence over K, V [H, L, 128]."""
+    u, n, L, G = 2.0 ** -11, len(q), K.shape[1], q.shape[1] // K.shape[0]
+    out, lse = np64(out), np64(lse)
+    z = np.abs(V.min(-1))
+    for i in range(n):
+        seen = L - n + i + 1
+        for h in range(q.shape[1]):
+            k, v, row = K[h // G, :seen], V[h // G, :seen], q[i, h].astype(np.float64)
+            qb, kb = (row, k) if not p.fd["k_rotate"] else (row @ WHT, k @ WHT)
+            # the group's other tokens share its scales, seen or not
+            every = K[h // G] if not p.fd["k_rotate"] else K[h // G] @ WHT
+            d = (2 * u + u * u) * scale * np.max(np.abs(every) @ np.abs(qb))
+            x = scale * kb @ qb
+            rl = x.max() + np.log(np.exp(x - x.max()).sum())
+            w = np.exp(x - rl)
+            want = w @ v
+            bar = ((1 + 2 * u) * (1 + 2.0 ** -16) * np.exp(2 * d) - 1) * (w @ (np.abs(v) + z[h // G, :seen, None])) + 1e-7
+            err = np.abs(out[i, h] - want)
+            assert np.all(err <= bar), (i, h, float(np.max(err / bar)))
+            assert abs(lse[i, h] - rl) <= d + 2.0 ** -16 * (1 + abs(rl)), (i, h)
+
+
+# ---- packed magnitudes beyond fp16 ------------------------------------------------------------
+@pytest.mark.parametrize("n", [4, 30, 200])      # 16 rows per KV head, 120, and 800
+@pytest.mark.parametrize("what", ["value", "key", "both", "fp16 value", "fp16 key"])
+def test_packed_magnitudes_beyond_fp16(n, what):
+    dt = F16 if what.startswith("fp16") else BF16
+    rng = np.random.default_rng(80)
+    k, v = normal(rng, (384, 2, 128), dt), normal(rng, (384, 2, 128), dt)
+    at = 382                                       # the last but one: few rows see it
+    if what in ("value", "both"):
+        v[at, :, 7] = synth.to_bf16_values(np.float32(150000))
+    if what in ("key", "both"):
+        k[at, :, 9] = synth.to_bf16_values(np.float32(900000))
+    if what == "fp16 value":
+        v[at, :, 7], v[at, :, 90] = TOP, -TOP       # 3 s + z = 65536
+    if what == "fp16 key":
+        k[at, :, 9], k[at - 1, :, 9] = TOP, -TOP    # 15 s + z = 65536
+    p = filled(fmt(n_sink=0, src_dtype=dt), k, v)
+    assert int(p.status) == 0                      # every scale and zero-point fits
+    K, V = serving.tokens(p.ora, 0, p.tq[0], p.tr[0])
+    assert max(K.max(), V.max()) > TOP
+    if n > 16:                                     # tiles of fp16 keys and values: the largest number stands in
+        K, V = np.minimum(K, TOP), np.minimum(V, TOP)
+    q, scale, out, lse = p.attend([n], 4, scale=2.0 ** -18)
+    assert int(p.status) == RANGE
+    assert torch.isfinite(out).all()
+    check_rows(p, q, scale, out, lse, K, V)
+
+
+@pytest.mark.parametrize("n", [4, 30, 200])
+@pytest.mark.parametrize("names", [("k_scale",), ("k_zero",), ("v_scale",), ("v_zero",), ("k_scale", "v_zero")])
+def test_packed_metadata_that_did_not_fit_counts_as_zero(n, names):
+    # an append of larger magnitudes yet (which raised KVQ_DEV_RANGE) leaves Inf in the metadata
+    rng = np.random.default_rng(81)
+    p = filled(fmt(n_sink=0), normal(rng, (384, 2, 128), BF16), normal(rng, (384, 2, 128), BF16))
+    K, V = serving.tokens(p.ora, 0, p.tq[0], p.tr[0])
+    for name in names:
+        sign = -1 if name.endswith("zero") else 1
+        p.gpu.pool.tensors[name].view(torch.float16).view(-1, 2, 128)[int(p.table[0, 2]), :, 126] = sign * float("inf")
+        if name[0] == "k":
+            K[:, 256:, 126] = 0
+        else:
+            V[:, 256 + 126] = 0
+    q, scale, out, lse = p.attend([n], 4)
+    assert int(p.status) == RANGE
+    check_rows(p, q, scale, out, lse, K, V)
