@@ -4,7 +4,7 @@
 // Mathematics.  Scores are products with tokens as M and query rows as N (m16n8k16, two of them for 16
 // rows), values with channels as M and query rows as N:
 //   A[t][d] = c[t][d] 2^-24 f_d   (a 4-bit code masked into the low bits of an fp16 number, f_d = 1 or 16),
-//   B[d][r] = fp16(q[r][d] s[d] / f_d)  per group,   score = 2^24 (A B) + sum_d (q z + 8 (q s - f_d B)),
+//   B[d][r] = fp16(q[r][d] s[d] / (f_d n))  per group,   score = 2^24 n (A B) + sum_d (q z + 8 (q s - f_d n B)),
 //   A[d][t] = c[t][d] exactly (masked into 2^k + c, less 2^k),   B[t][r] = fp16(p s 2^7),
 //   O[d][r] = 2^-7 (A B) + sum_t p z.
 // A lane's four words of a key row are the A fragments of eight k-steps (channels go to k in the order that the
@@ -12,7 +12,9 @@
 // (tile c: channels 8 g + c and 64 + 8 g + c).  The probabilities go from one product to the other by an 8x8
 // transpose in registers.  The running maximum follows score + log2 s, which keeps B inside fp16 for any
 // scale; it moves only when exceeded by more than 8.  Queries are scaled to [4, 8) by a power of two of their
-// row: with key scales up to 65504 / 15 the products stay below 65504.
+// row, and n is 1 but for groups with a key scale above 8188 (65504 / 8), where 8 times the scale would leave fp16:
+// there n = 16, which serves up to fp16's largest scale.  A smaller range of the queries would serve all
+// groups, but costs small scales their last bits: q s / 16 is subnormal below 2^-14.
 //
 // What bounds it: the expansion and the softmax on CUDA cores (about 200 instructions per 16 tokens and warp);
 // the packed bytes pass once per 16 rows.  4 tokens x 8 sequences over 32768 and fewer, 8 x 4 heads: 99 us, of
@@ -50,6 +52,10 @@ __device__ __forceinline__ uint32_t h2mul(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
+}
+constexpr uint32_t kSixteenth2 = 0x2C002C00u;
+__device__ __forceinline__ uint32_t at_most_8188(uint32_t s) {   // all ones in such halves
+  return __hle2_mask(*reinterpret_cast<const __half2*>(&s), __half2half2(__ushort_as_half(0x6FFF)));
 }
 __device__ __forceinline__ float2 h2f(uint32_t a) { return __half22float2(*reinterpret_cast<const __half2*>(&a)); }
 
@@ -160,23 +166,30 @@ __device__ __forceinline__ void value_tile(State& st, int c, const uint32_t (&w)
 }
 
 // A group's metadata, four channels and four tokens a lane: what gives numbers beyond fp16 is flagged, and key
-// channels with an infinity or NaN are set to zero where they lie (value tokens are as they are read).
-__device__ __forceinline__ void check_group(uint8_t* in, int lane, int valid, int& flags) {
+// channels with an infinity or NaN are set to zero where they lie (value tokens are as they are read).  With
+// a scale above 8188 all key scales are divided by n = 16 there; true then.
+__device__ __forceinline__ bool check_group(uint8_t* in, int lane, int valid, int& flags) {
   uint2* ks = reinterpret_cast<uint2*>(in + kKMeta) + lane;
   uint2* kz = reinterpret_cast<uint2*>(in + kKMeta + 256) + lane;
   const uint2 vs = reinterpret_cast<const uint2*>(in + kVMeta)[lane], vz = reinterpret_cast<const uint2*>(in + kVMeta + 256)[lane];
-  const uint2 s = *ks, z = *kz;
+  uint2 s = *ks, z = *kz;
   const int left = valid - 4 * lane;
   const uint32_t k = finite2(h2fma(kFifteen2, s.x, z.x)) & finite2(h2fma(kFifteen2, s.y, z.y));
   const uint32_t v = (finite2(h2fma(kThree2, vs.x, vz.x)) | (left >= 2 ? 0u : left == 1 ? 0xffff0000u : 0xffffffffu)) &
                      (finite2(h2fma(kThree2, vs.y, vz.y)) | (left >= 4 ? 0u : left == 3 ? 0xffff0000u : 0xffffffffu));
-  if (!__any_sync(0xffffffffu, (k & v) != 0xffffffffu)) return;
+  const uint32_t small = at_most_8188(s.x) & at_most_8188(s.y);
+  if (!__any_sync(0xffffffffu, (k & v & small) != 0xffffffffu)) return false;
   if ((k & v) != 0xffffffffu) flags |= KVQ_DEV_RANGE;
   const uint32_t mx = finite2(s.x) & finite2(z.x), my = finite2(s.y) & finite2(z.y);
-  *ks = make_uint2(s.x & mx, s.y & my);
-  *kz = make_uint2(z.x & mx, z.y & my);
+  s = make_uint2(s.x & mx, s.y & my);
+  z = make_uint2(z.x & mx, z.y & my);
+  const bool big = __any_sync(0xffffffffu, (at_most_8188(s.x) & at_most_8188(s.y)) != 0xffffffffu);
+  if (big) s = make_uint2(h2mul(s.x, kSixteenth2), h2mul(s.y, kSixteenth2));
+  *ks = s;
+  *kz = z;
   fence_async_smem();   // before the next group's copies into this stage
   __syncwarp();
+  return big;
 }
 
 __global__ void __launch_bounds__(32 * kWarps, 1) attn_narrow_kernel(const __grid_constant__ AttnArgs a,
@@ -394,7 +407,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_narrow_kernel(const __gri
           ++taken;
           uint8_t* in = stages + slot * kStage;
           const int valid = min(128, c.tq - 128 * gi);
-          check_group(in, lane, valid, flags);
+          const float by = check_group(in, lane, valid, flags) ? 16.0f : 1.0f;   // n
           // this group's B fragments and zero-point sums
           uint32_t bs[2][16];
           float mul[4], add[4], zd[2] = {0.0f, 0.0f};
@@ -414,8 +427,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_narrow_kernel(const __gri
                 bs[n][4 * k + j] = h2mul(qp[n][4 * k + j], sp[j]);
                 // q z, and what the rounding of q s takes from a code of 8, so that the error goes with c - 8
                 const float2 bf = h2f(bs[n][4 * k + j]);
-                const float ex = fmaf(8.0f, fmaf(qf.x, sf.x, -bf.x), qf.x * zf.x);
-                const float ey = fmaf(8.0f, fmaf(qf.y, sf.y, -bf.y), qf.y * zf.y);
+                const float ex = fmaf(8.0f * by, fmaf(qf.x, sf.x, -bf.x), qf.x * zf.x);
+                const float ey = fmaf(8.0f * by, fmaf(qf.y, sf.y, -bf.y), qf.y * zf.y);
                 zd[n] = fmaf(f, ex + ey, zd[n]);
               }
             }
@@ -430,7 +443,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_narrow_kernel(const __gri
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             add[q] = cs[q] * __shfl_sync(0xffffffffu, zd[q >> 1], 4 * (2 * t + (q & 1)));
-            mul[q] = cs[q] * 16777216.0f;
+            mul[q] = cs[q] * (16777216.0f * by);
             cols[q] = see[q].packed - 128 * gi;
             edge |= cols[q] < 128;
           }

@@ -104,3 +104,55 @@ def test_packed_metadata_that_did_not_fit_counts_as_zero(n, names):
     q, scale, out, lse = p.attend([n], 4)
     assert int(p.status) == RANGE
     check_rows(p, q, scale, out, lse, K, V)
+
+
+# ---- key scales near fp16's end ------------------------------------------------------------------
+@pytest.mark.parametrize("n", [1, 4, 30, 200])
+@pytest.mark.parametrize("kw", [dict(), dict(src_dtype=F16), dict(src_dtype=F16, k_rotate=1)])
+@pytest.mark.parametrize("c", range(8))
+def test_key_scales_near_the_end_of_fp16(n, kw, c):
+    # a channel from -62000 to 62000 has scale 8267; every number stays inside fp16
+    fd = fmt(**dict(dict(n_sink=0), **kw))
+    dt = fd["src_dtype"]
+    rng = np.random.default_rng(82)
+    k, v = normal(rng, (384, 2, 128), dt), normal(rng, (384, 2, 128), dt)
+    if fd["k_rotate"]:
+        e = np.zeros(128)
+        e[c] = 62000
+        row = synth.to_dtype_values((e @ WHT).astype(np.float32), dt)
+        k[380], k[381] = row, -row
+    else:
+        k[380, :, c], k[381, :, c] = synth.to_dtype_values(np.float32(62000), dt), synth.to_dtype_values(np.float32(-62000), dt)
+    p = filled(fd, k, v)
+    assert int(p.status) == 0
+    K, V = serving.tokens(p.ora, 0, p.tq[0], p.tr[0])
+    q = normal(rng, (n, 8, 128), BF16)
+    if fd["k_rotate"]:
+        e[c] = 7.96875
+        q = synth.to_bf16_values((0.01 * q + e @ WHT).astype(np.float32))
+    else:
+        q[:, :, c] = 7.96875                       # just below a power of two, the row's largest
+    q, scale, out, lse = p.attend([n], 4, scale=2.0 ** -16, q=q)
+    assert int(p.status) == 0
+    check_rows(p, q, scale, out, lse, K, V)
+
+
+@pytest.mark.parametrize("n", [1, 4, 16])
+@pytest.mark.parametrize("top", [100000.0, 300000.0, 600000.0, 940000.0])
+@pytest.mark.parametrize("kw", [dict(), dict(src_dtype=F32)])
+def test_key_scales_up_to_the_end_of_fp16(n, top, kw):
+    # all eight channels of an octet, some with small scales beside them; at most 64 rows take packed keys as they are
+    fd = fmt(n_sink=0, **kw)
+    dt = fd["src_dtype"]
+    rng = np.random.default_rng(86)
+    k, v = normal(rng, (384, 2, 128), dt), normal(rng, (384, 2, 128), dt)
+    k[300, :, 8:16] = synth.to_dtype_values(np.float32(top), dt)
+    k[:, :, 16:64] *= np.float32(2.0 ** -12)
+    p = filled(fd, k, v)
+    assert int(p.status) == 0
+    K, V = serving.tokens(p.ora, 0, p.tq[0], p.tr[0])
+    q = normal(rng, (n, 8, 128), BF16)
+    q[:, ::2, 8:16] = 7.96875
+    q, scale, out, lse = p.attend([n], 4, scale=2.0 ** -20, q=q)
+    assert int(p.status) == RANGE
+    check_rows(p, q, scale, out, lse, K, V)
