@@ -613,7 +613,8 @@ size_t kvq_attention_paged_workspace_bytes(const kvq_format* fmt, int32_t num_se
  * once (for a few rows: query times key scale, and probability times value scale).  Keys
  * and values that fp16 does not hold, in the tokens that a block of rows reads: a NaN or Inf
  * raw one raises KVQ_DEV_NONFINITE and counts as 0; a raw one beyond +-65504 raises
- * KVQ_DEV_RANGE and counts as 0; packed ones whose scale or zero-point did not fit fp16 at
+ * KVQ_DEV_RANGE and counts as 0 (a number beyond it that the transform of a k_rotate format
+ * makes of a raw key raises it too and counts as +-65504); packed ones whose scale or zero-point did not fit fp16 at
  * their append raise KVQ_DEV_RANGE and count as 0 (a key channel of its group, a value
  * token); packed ones of a fitting scale and zero-point whose largest code gives more than
  * 65504 raise KVQ_DEV_RANGE, and numbers beyond it count as 65504 (for a few rows, at most

@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attn_narrow_kernel(const __gri
               if (a.L.k_rotate) {
                 wht_quarter(x[n], lane, a.L.rot_scale);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) x[n][j] = fminf(fmaxf(x[n][j], -65504.0f), 65504.0f);
+                for (int j = 0; j < 32; ++j) x[n][j] = within_f16(x[n][j], flags);
               }
             }
             const uint32_t sixteen = 0x4C004C00u;

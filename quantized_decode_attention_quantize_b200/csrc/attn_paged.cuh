@@ -377,6 +377,12 @@ __device__ __forceinline__ void raw8(const AttnArgs& a, int64_t slab, int count,
     }
   }
 }
+// A raw key in the transformed basis, up to sqrt(128) times the row's largest magnitude: as the largest fp16 number
+// of its sign where fp16 does not hold it, which is flagged.
+__device__ __forceinline__ float within_f16(float x, int& flags) {
+  if (fabsf(x) > 65504.0f) flags |= KVQ_DEV_RANGE;
+  return fminf(fmaxf(x, -65504.0f), 65504.0f);
+}
 __device__ __forceinline__ int put_raw_k(const AttnArgs& a, int64_t slab, int count, int ns, int r0, uint32_t slot, int t) {
   int flags = 0;
   const int o = t & 15;
@@ -388,7 +394,7 @@ __device__ __forceinline__ int put_raw_k(const AttnArgs& a, int64_t slab, int co
     if (a.L.k_rotate) {   // packed keys and the queries are in the transformed basis
       wht128_octet_unscaled(x, t & 31);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = fminf(fmaxf(x[e] * a.L.rot_scale, -65504.0f), 65504.0f);
+      for (int e = 0; e < 8; ++e) x[e] = within_f16(x[e] * a.L.rot_scale, flags);
     }
     st16(slot + (o >> 3) * 16384 + r * 128 + (((o & 7) ^ (r & 7)) << 4), pack_f16(x[0], x[4]), pack_f16(x[1], x[5]),
          pack_f16(x[2], x[6]), pack_f16(x[3], x[7]));

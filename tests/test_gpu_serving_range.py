@@ -156,3 +156,30 @@ def test_key_scales_up_to_the_end_of_fp16(n, top, kw):
     q, scale, out, lse = p.attend([n], 4, scale=2.0 ** -20, q=q)
     assert int(p.status) == RANGE
     check_rows(p, q, scale, out, lse, K, V)
+
+
+# ---- raw rows of a transforming format ------------------------------------------------------------
+@pytest.mark.parametrize("n", [4, 30, 100])
+@pytest.mark.parametrize("where", ["window", "sink"])
+def test_raw_keys_that_leave_fp16_in_the_transformed_basis(n, where):
+    # a constant row has sqrt(128) times its magnitude in one channel of the transform
+    rng = np.random.default_rng(83)
+    ns = 0 if where == "window" else 120
+    k, v = normal(rng, (110, 2, 128), F16), normal(rng, (110, 2, 128), F16)
+    p = Paged(fmt(n_sink=ns, src_dtype=F16, k_rotate=1), 2, 1, 3, seed=3)
+    tr0 = -ns
+    for rows in ("clean", "large"):
+        if rows == "large":
+            k[109] = 60000
+        out = ints([0]), ints([0])
+        kvq.append_paged(p.fmt, p.gpu, ints([0, 110]), 110, ints([0]), ints([tr0]), dev(k, F16), dev(v, F16), *out)
+        p.tq, p.tr = [0], out[1].tolist()
+        if rows == "clean":
+            q, scale, clean, _ = p.attend([n], 4, scale=2.0 ** -16)
+            assert int(p.status) == 0
+        else:
+            _, _, out, lse = p.attend([n], 4, scale=2.0 ** -16, q=q)
+    assert int(p.status) == RANGE
+    assert torch.equal(out[:n - 1], clean[:n - 1])
+    T = np.clip(k.astype(np.float64) @ WHT, -TOP, TOP) @ WHT
+    check_rows(p, q, scale, out, lse, T.swapaxes(0, 1), v.astype(np.float64).swapaxes(0, 1))
