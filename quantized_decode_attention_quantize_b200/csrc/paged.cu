@@ -106,25 +106,25 @@ __device__ __forceinline__ Octet<DT> octet_put(const float (&f)[8]) {   // round
 
 // Codes of eight values, BITS each, packed from the low end: rint_even(fl(fl(x - z) / s)) as pack8 finds it (the
 // product with fl(1 / s) decides unless it lies within 2^-12 of a half-integer).  0 <= x - z and s is rounded
-// up, so the quotient stays within half a step of 0 .. 2^BITS - 1 and needs no clamp.  q + 1.5 * 2^23 holds
-// the integer in its low bits; the sums of these words, less the constants, are the packed codes.
+// up, so the quotient stays within half a step of 0 .. 2^BITS - 1 and needs no clamp; where x, s or z is
+// not finite it is NaN (or 0), and the code 0 as pack8's.  q + 1.5 * 2^23 holds the integer in its low bits; the
+// sums of these words, less the constants, are the packed codes, so no word may hold anything else.
 template <int BITS>
 __device__ __forceinline__ uint32_t pack_codes(const float (&x)[8], const float (&s)[8], const float (&rs)[8],
                                                const float (&z)[8]) {
   const float big = 12582912.0f;
   float q[8], t[8];
-  bool near = false;
+  bool near = false;   // or NaN
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     q[j] = __fmul_rn(__fsub_rn(x[j], z[j]), rs[j]);
     t[j] = __fadd_rn(q[j], big);
-    near |= fabsf(__fsub_rn(q[j], __fsub_rn(t[j], big))) > 0.5f - 0x1p-12f;
+    near |= !(fabsf(__fsub_rn(q[j], __fsub_rn(t[j], big))) <= 0.5f - 0x1p-12f);
   }
   if (near) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (fabsf(__fsub_rn(q[j], __fsub_rn(t[j], big))) > 0.5f - 0x1p-12f)
-        t[j] = __fadd_rn(__fdiv_rn(__fsub_rn(x[j], z[j]), s[j]), big);
+    for (int j = 0; j < 8; ++j)   // NaN becomes code 0
+      t[j] = fmaxf(__fadd_rn(__fdiv_rn(__fsub_rn(x[j], z[j]), s[j]), big), big);
   }
   uint32_t w = 0, less = 0;
 #pragma unroll

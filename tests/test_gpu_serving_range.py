@@ -183,3 +183,49 @@ def test_raw_keys_that_leave_fp16_in_the_transformed_basis(n, where):
     assert torch.equal(out[:n - 1], clean[:n - 1])
     T = np.clip(k.astype(np.float64) @ WHT, -TOP, TOP) @ WHT
     check_rows(p, q, scale, out, lse, T.swapaxes(0, 1), v.astype(np.float64).swapaxes(0, 1))
+
+
+# ---- the append's codes ------------------------------------------------------------------------------
+@pytest.mark.parametrize("dt", [F32, BF16, F16])
+@pytest.mark.parametrize("bad", [-100000.0, 2000000.0, float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("rotate", [0, 1])
+def test_appended_groups_equal_the_quantizers_whatever_they_hold(dt, bad, rotate):
+    # one key channel and one value token that do not fit (or are no numbers): the other channels and
+    # tokens must not notice, and a group appended holds what kvq_quantize_kv_paged packs
+    if dt == F16 and np.isfinite(bad):
+        bad = float(np.sign(bad)) * TOP            # all that the type has; it fits
+    rng = np.random.default_rng(84)
+    k, v = normal(rng, (128, 2, 128), dt), normal(rng, (128, 2, 128), dt)
+    clean = k.copy(), v.copy()
+    k[40, :, 9] = v[41, :, 70] = bad
+    pools = []
+    for ks, vs in ((k, v), clean):
+        p = Paged(fmt(n_sink=0, src_dtype=dt, k_rotate=rotate), 2, 1, 2, seed=4, spare=2)
+        out = ints([0]), ints([0])
+        kvq.append_paged(p.fmt, p.gpu, ints([0, 128]), 128, ints([0]), ints([0]), dev(ks, dt), dev(vs, dt), *out,
+                         status=p.status)
+        assert out[0].tolist() == [128] and out[1].tolist() == [0]
+        blk, other = int(p.table[0, 0]), int(p.table[0, 1])
+        st = status0()
+        kvq.quantize_kv_paged(p.fmt, p.gpu, dev(ks, dt).transpose(0, 1)[None], dev(vs, dt).transpose(0, 1)[None],
+                              ints([other]), 128, status=st)
+        assert int(st) == int(p.status)
+        pools.append([p.gpu.pool.tensors[n].view(p.gpu.num_blocks, 2, -1)[[blk, other]].cpu().numpy() for n in POOL])
+    fits = dt == F16 and np.isfinite(bad)
+    assert (int(p.status) == 0) and (fits or not np.array_equal(pools[0][0], pools[1][0]))
+    for name, got, same in zip(POOL, *pools):
+        np.testing.assert_array_equal(got[0], got[1], err_msg=name)
+        if rotate and name[0] == "k":
+            continue                               # the transform spreads a row's element over its channels
+        a, b = got[0], same[0]                     # [head, bytes]: keys by channel, values by token
+        if name == "k_codes":
+            keep = np.ones((128, 64), bool)
+            keep[:, 4] = False                     # channels 8 and 9 share a byte
+            a, b = (x.reshape(2, 128, 64)[:, keep] for x in (a, b))
+            hi = [x[0].reshape(2, 128, 64)[:, :, 4] & 15 for x in (got, same)]
+            np.testing.assert_array_equal(*hi)
+        elif name == "v_codes":
+            a, b = (np.delete(x.reshape(2, 64, 64), 20, 1) for x in (a, b))   # tokens 40 and 41 share words
+        else:
+            a, b = (np.delete(x.view(np.float16), 9 if name[0] == "k" else 41, 1) for x in (a, b))
+        np.testing.assert_array_equal(a, b, err_msg=name)
