@@ -32,6 +32,7 @@ ARRAYS = [
     "sink_k", "sink_v", "res_k", "res_v",
     "v_sketch",
 ]
+RAW_ARRAYS = ("sink_k", "sink_v", "res_k", "res_v")
 
 TORCH_DTYPE = {F32: torch.float32, F16: torch.float16, BF16: torch.bfloat16}
 KVQ_DTYPE = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
@@ -182,10 +183,25 @@ def kqv_codebook(bits: int, head_dim: int):
     return list(out)
 
 
+def _given(fmt, name, t, need, device):
+    """Checks a caller's tensor for the array `name` of `need` bytes: kernels get its bare address."""
+    if t is None or not t.is_contiguous() or t.numel() * t.element_size() != need:
+        raise ValueError(f"{name}: a contiguous tensor of {need} bytes is needed")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, the cache's other arrays on {device}")
+    if t.is_floating_point():
+        own = (TORCH_DTYPE[fmt.src_dtype],) if name in RAW_ARRAYS else () if "code" in name else (torch.float16, torch.float32)
+        if t.dtype not in own:
+            raise ValueError(f"{name}: {t.dtype} is not the array's type")
+    if t.data_ptr() % 16:
+        raise ValueError(f"{name}: must start on a 16-byte boundary")
+
+
 class Cache:
     """Device arrays of a packed cache (torch uint8 tensors), owned by this object.
     k_lut / v_lut: the codebooks (NUQ: stored as fp16, KQV: fp32); sketch: the KQV sketch
-    matrix [D][D] (stored as fp32)."""
+    matrix [D][D] (stored as fp32).  arrays: name -> the caller's tensor, used in place of new
+    ones (all that the format needs; checked as PagedCache's)."""
 
     def __init__(self, fmt: kvq_format, B: int, H: int, C: int, device="cuda", k_lut=None,
                  v_lut=None, sketch=None, arrays=None):
@@ -193,9 +209,12 @@ class Cache:
         self.tensors = {}
         self.struct = kvq_cache(batch=B, kv_heads=H, capacity=C)
         if arrays is not None:   # the caller's tensors
-            self.tensors.update(arrays)
             for name, t in arrays.items():
+                if name not in ARRAYS:
+                    raise ValueError(f"{name}: not an array of a cache")
+                _given(fmt, name, t, cache_array_bytes(fmt, B, H, C, ARRAYS.index(name)), next(iter(arrays.values())).device)
                 setattr(self.struct, name, t.data_ptr())
+            self.tensors.update(arrays)
             return
         for i, name in enumerate(ARRAYS):
             n = cache_array_bytes(fmt, B, H, C, i)
@@ -382,22 +401,23 @@ class PagedCache:
 
     def __init__(self, fmt: kvq_format, kv_heads: int, num_blocks: int, num_seqs: int, max_blocks: int,
                  device="cuda", arrays=None):
-        """arrays: name -> contiguous device tensor of the array's bytes (block_table: int32
-        [num_seqs][max_blocks]), used in place of new zeroed ones; they stay the caller's."""
+        """arrays: name -> contiguous tensor of the array's bytes, 16-byte aligned, in its own type or one of
+        integers, all on the device of block_table (int32 [num_seqs][max_blocks]); used in place
+        of new zeroed ones, they stay the caller's."""
         self.fmt, self.H, self.num_blocks = fmt, kv_heads, num_blocks
         self.num_seqs, self.max_blocks = num_seqs, max_blocks
         if arrays is None:
             self.pool = Cache(fmt, num_blocks, kv_heads, fmt.group_tokens, device=device)
             raw = Cache(fmt, num_seqs, kv_heads, fmt.group_tokens, device=device)
-            self.raw = {n: raw.tensors[n] for n in ("sink_k", "sink_v", "res_k", "res_v") if n in raw.tensors}
+            self.raw = {n: raw.tensors[n] for n in RAW_ARRAYS if n in raw.tensors}
             self.block_table = torch.full((num_seqs, max_blocks), -1, dtype=torch.int32, device=device)
         else:
+            self.block_table = arrays.get("block_table")
+            if self.block_table is None or self.block_table.dtype != torch.int32 or \
+                    tuple(self.block_table.shape) != (num_seqs, max_blocks) or not self.block_table.is_contiguous():
+                raise ValueError("block_table must be a contiguous int32 [num_seqs][max_blocks]")
             self.pool = Cache(fmt, num_blocks, kv_heads, fmt.group_tokens, arrays=self._part(arrays, False, num_blocks))
             self.raw = self._part(arrays, True, num_seqs)
-            self.block_table = arrays["block_table"]
-            if self.block_table.dtype != torch.int32 or tuple(self.block_table.shape) != (num_seqs, max_blocks) or \
-                    not self.block_table.is_contiguous():
-                raise ValueError("block_table must be a contiguous int32 [num_seqs][max_blocks]")
         self.device = self.block_table.device
         self.struct = kvq_paged_cache(pool=self.pool.struct, num_seqs=num_seqs, max_blocks=max_blocks,
                                       block_table=self.block_table.data_ptr())
@@ -405,17 +425,16 @@ class PagedCache:
             setattr(self.struct, n, t.data_ptr())
 
     def _part(self, arrays, per_seq, slabs):
-        """The given pool (or per-sequence raw) arrays, each of the size the format asks for."""
+        """The given pool (or per-sequence raw) arrays that the format needs, checked."""
         got = {}
         for i, n in enumerate(ARRAYS):
-            if (n in ("sink_k", "sink_v", "res_k", "res_v")) != per_seq:
+            if (n in RAW_ARRAYS) != per_seq:
                 continue
             need = cache_array_bytes(self.fmt, slabs, self.H, self.fmt.group_tokens, i)
             if not need:
                 continue
             t = arrays.get(n)
-            if t is None or not t.is_contiguous() or t.numel() * t.element_size() != need:
-                raise ValueError(f"{n}: a contiguous tensor of {need} bytes is needed")
+            _given(self.fmt, n, t, need, self.block_table.device)
             got[n] = t
         return got
 
@@ -429,6 +448,7 @@ class PagedCache:
 def quantize_kv_paged(fmt, cache: PagedCache, k_src: torch.Tensor, v_src: torch.Tensor, blocks: torch.Tensor,
                       n: int, status=None, stream=None):
     """kvq_quantize_kv_paged: k_src, v_src [num_seqs, H, n, D]; blocks int32 [num_seqs] (device)."""
+    _need(cache.device.type == "cuda", "the cache must be on a CUDA device")
     if k_src.stride() != v_src.stride():
         raise ValueError("k_src and v_src must have the same strides")
     st = lib().kvq_quantize_kv_paged(ctypes.byref(fmt), cache.ref(), _ptr(k_src), _ptr(v_src), k_src.stride(0),
@@ -445,6 +465,7 @@ def decode_attention_paged(fmt, cache: PagedCache, t_quant: torch.Tensor, t_res:
                            max_t_res: int, q: torch.Tensor, scale: float, out_dtype=F32, out=None, workspace=None,
                            status=None, stream=None):
     """kvq_decode_attention_paged: t_quant, t_res int32 [num_seqs] (device); q [num_seqs, Hq, D]."""
+    _need(cache.device.type == "cuda", "the cache must be on a CUDA device")
     S, Hq, D = q.shape
     if out is None:
         out = torch.empty((S, Hq, D), dtype=TORCH_DTYPE[out_dtype], device=q.device)
