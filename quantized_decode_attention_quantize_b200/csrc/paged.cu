@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 4) read_paged_kernel(const __grid_co
   const ReadSeq q = read_seq(a, s);
   if (unit > q.ng + 1) return;
   if (!q.ok) {
-    if (unit == 0 && blockIdx.y == 0 && threadIdx.x == 0) flag(a.status, KVQ_DEV_BOUNDS);
+    if (unit == 0 && h == 0 && threadIdx.x == 0) flag(a.status, KVQ_DEV_BOUNDS);   // either side may be the only one
     return;
   }
   const int o = threadIdx.x & 15, rs = threadIdx.x >> 4, lane = threadIdx.x & 31;

@@ -634,23 +634,27 @@ def append_paged(fmt, cache: PagedCache, cu_new: torch.Tensor, max_new: int, t_q
 
 
 def read_paged(fmt, cache: PagedCache, cu: torch.Tensor, max_rows: int, first: torch.Tensor, t_quant: torch.Tensor,
-               t_res: torch.Tensor, n_rows: int, out_dtype=None, k_out=None, v_out=None, status=None, stream=None):
+               t_res: torch.Tensor, n_rows: int, out_dtype=None, k_out=None, v_out=None, status=None, stream=None,
+               keys=True, values=True):
     """kvq_read_paged: the tokens at positions first[s], ... of every sequence as rows
-    [cu[s], cu[s + 1]) -> k, v [n_rows, Hkv, D] (out_dtype: the source dtype by default)."""
+    [cu[s], cu[s + 1]) -> k, v [n_rows, Hkv, D] (out_dtype: the source dtype by default); a side that is not
+    wanted (keys / values = False) is None."""
     d = cache.device
     out_dtype = fmt.src_dtype if out_dtype is None else out_dtype
     shape, dt = (n_rows, cache.H, fmt.head_dim), TORCH_DTYPE[out_dtype]
     cu, tq, tr = _batch(cache, cu, t_quant, t_res)
     p0 = _ints(first, cache.num_seqs, d, "first")
-    for x in (k_out, v_out):
-        if x is not None and (x.shape != shape or x.dtype != dt or x.device != d or not x.is_contiguous()):
-            raise ValueError("k_out / v_out: contiguous [n_rows, kv_heads, head_dim] in out_dtype is needed")
+    for x, wanted in ((k_out, keys), (v_out, values)):
+        if x is not None and (not wanted or x.shape != shape or x.dtype != dt or x.device != d or not x.is_contiguous()):
+            raise ValueError("k_out / v_out: contiguous [n_rows, kv_heads, head_dim] in out_dtype is needed, for a side that is read")
+    _need(keys or values, "keys or values are needed")
 
     def body(s):
-        k = torch.empty(shape, dtype=dt, device=d) if k_out is None else k_out
-        v = torch.empty(shape, dtype=dt, device=d) if v_out is None else v_out
-        _check("kvq_read_paged", lib().kvq_read_paged(fmt, cache.struct, cu, n_rows, max_rows, p0, tq, tr, k.data_ptr(),
-                                                      v.data_ptr(), out_dtype, _status_ptr(status, d), s))
+        k = torch.empty(shape, dtype=dt, device=d) if keys and k_out is None else k_out
+        v = torch.empty(shape, dtype=dt, device=d) if values and v_out is None else v_out
+        _check("kvq_read_paged", lib().kvq_read_paged(
+            fmt, cache.struct, cu, n_rows, max_rows, p0, tq, tr, None if k is None else k.data_ptr(),
+            None if v is None else v.data_ptr(), out_dtype, _status_ptr(status, d), s))
         return k, v
     return _on(d, stream, body)
 

@@ -229,3 +229,46 @@ def test_appended_groups_equal_the_quantizers_whatever_they_hold(dt, bad, rotate
         else:
             a, b = (np.delete(x.view(np.float16), 9 if name[0] == "k" else 41, 1) for x in (a, b))
         np.testing.assert_array_equal(a, b, err_msg=name)
+
+
+# ---- one side read back -------------------------------------------------------------------------------
+@pytest.mark.parametrize("side", ["k", "v"])
+@pytest.mark.parametrize("long", [False, True])
+def test_read_of_one_side_raises_what_both_raise(side, long):
+    p = Paged(fmt(), 2, 3, 3, seed=14)
+    p.append([200, 150, 10])
+    n = 140 if long else 100
+
+    def read(tq, first):
+        cu, first, tq, tr = ints([0, n, 2 * n, 2 * n + 5]), ints(first), ints(tq), ints(p.tr)
+        out = torch.full((3 * n, 2, 128), 3.0, device="cuda", dtype=torch.bfloat16)
+        p.status.zero_()
+        args = [out.data_ptr(), None] if side == "k" else [None, out.data_ptr()]
+        st = kvq.lib().kvq_read_paged(ctypes.byref(p.fmt), p.gpu.ref(), kvq._ptr(cu), 3 * n, n, kvq._ptr(first),
+                                      kvq._ptr(tq), kvq._ptr(tr), *args, BF16, kvq._ptr(p.status), None)
+        torch.cuda.synchronize()
+        assert st == kvq.KVQ_OK
+        return out, int(p.status)
+
+    want = [serving.tokens(p.ora, s, p.tq[s], p.tr[s])[side == "v"] for s in range(3)]
+
+    def rows(s, lo, m):
+        return serving.round_src(want[s][:, lo:lo + m].swapaxes(0, 1), BF16)
+
+    out, st = read(p.tq, [3, 4, 2])
+    assert st == 0
+    for s, (lo, m) in enumerate(((3, n), (4, n), (2, 5))):
+        np.testing.assert_array_equal(np64(out[s * n:s * n + m]), rows(s, lo, m))
+    assert torch.all(out[2 * n + 5:] == 3.0)
+    for tq, first in ((p.tq, [3, 200, 2]), ([p.tq[0], -5, p.tq[2]], [3, 4, 2])):   # tokens it does not hold; a bad length
+        out, st = read(tq, first)
+        assert st == BOUNDS
+        np.testing.assert_array_equal(np64(out[:n]), rows(0, 3, n))
+        assert torch.all(out[n:2 * n] == 3.0)
+        np.testing.assert_array_equal(np64(out[2 * n:2 * n + 5]), rows(2, 2, 5))
+    # the wrapper reads one side of the same rows
+    args = (p.fmt, p.gpu, ints([0, n, 2 * n, 2 * n + 5]), n, ints([3, 4, 2]), ints(p.tq), ints(p.tr), 2 * n + 5)
+    got = kvq.read_paged(*args, keys=side == "k", values=side == "v")
+    both = kvq.read_paged(*args)
+    i = "kv".index(side)
+    assert got[1 - i] is None and torch.equal(got[i], both[i])
