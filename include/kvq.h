@@ -563,7 +563,8 @@ kvq_status kvq_norm_rope(int32_t head_dim, int32_t dtype, int64_t n_tokens, cons
  * rope (nullable) turns the new keys on the way at their positions, or at positions[row]
  * when `positions` (device int32 [n_rows]) is given; the turned key is rounded to
  * src_dtype before it is stored or packed, so a token is packed from the same bits whether
- * or not it passed through the window.  Packed groups equal kvq_quantize_kv_paged's.
+ * or not it passed through the window.  Where the turn takes a finite key beyond
+ * src_dtype (by up to sqrt 2 and the table's amplitude) KVQ_DEV_RANGE is raised.  Packed groups equal kvq_quantize_kv_paged's.
  * max_new: host bound on the new tokens of one sequence.  A sequence is left as it was, its
  * lengths copied and KVQ_DEV_BOUNDS raised, when its rows or lengths are out of range, it
  * brings more than max_new tokens, t_quant[s] is not a multiple of group_tokens, or a block

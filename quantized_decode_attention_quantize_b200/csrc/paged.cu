@@ -135,9 +135,30 @@ __device__ __forceinline__ uint32_t pack_codes(const float (&x)[8], const float 
   return w - less;
 }
 
+// Whether an octet holds a NaN or Inf (0 times it is NaN), two 16-bit numbers at a time.
+template <int DT>
+__device__ __forceinline__ bool octet_bad(const Octet<DT>& x) {
+  if constexpr (DT == KVQ_F32) {
+    float fin = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) fin = fmaf(__uint_as_float(x.w[j]), 0.0f, fin);
+    return !(fin == 0.0f);
+  } else {
+    uint32_t fin = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (DT == KVQ_F16) asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(fin) : "r"(x.w[j]), "r"(0));
+      else asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(fin) : "r"(x.w[j]), "r"(0));
+    }
+    return (fin & 0x7fff7fffu) != 0;
+  }
+}
+
 // Octet o of N rows, those with fresh[k] being new tokens (row `row[k]` of the source, at position pos[k]),
-// checked, and when they are keys turned and rounded.  The 16 lanes of a row call together: the
-// half-layout partner comes from its lane.
+// when they are keys turned and rounded, and checked as they are stored.  The 16 lanes of a row call together: the
+// half-layout partner comes from its lane.  A NaN or Inf stays one when it is turned, so the check of what is
+// stored finds it as well as numbers that the turn, up to sqrt 2 in magnitude, takes beyond the type; then the
+// octets it came from tell the two apart.
 template <int DT, int N>
 __device__ __forceinline__ void turn_rows(const AppendArgs& a, int which, int o, const int64_t (&row)[N],
                                           const int64_t (&pos)[N], const bool (&fresh)[N], Octet<DT> (&x)[N], int& flags) {
@@ -151,23 +172,28 @@ __device__ __forceinline__ void turn_rows(const AppendArgs& a, int which, int o,
       for (int j = 0; j < (DT == KVQ_F32 ? 8 : 4); ++j) y.w[j] = __shfl_sync(0xffffffffu, x[k].w[j], po, 16);
     }
     if (!fresh[k]) continue;
-    float f[8], fin = 0.0f;
-    octet_get<DT>(x[k], f);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) fin = fmaf(f[j], 0.0f, fin);
-    if (!(fin == 0.0f)) flags |= KVQ_DEV_NONFINITE;
-    if (!turns || 8 * o >= a.rope.rot) continue;
-    const int64_t at = a.positions ? a.positions[row[k]] : pos[k];
-    if (at < 0 || at >= a.rope.n_pos) {
-      flags |= KVQ_DEV_BOUNDS;
+    int64_t at = -1;
+    bool turned = turns && 8 * o < a.rope.rot;
+    if (turned) {
+      at = a.positions ? a.positions[row[k]] : pos[k];
+      if (at < 0 || at >= a.rope.n_pos) {
+        flags |= KVQ_DEV_BOUNDS;
+        turned = false;
+      }
+    }
+    if (!turned) {
+      if (octet_bad<DT>(x[k])) flags |= KVQ_DEV_NONFINITE;
       continue;
     }
-    float p[8];
+    float f[8], p[8];
+    octet_get<DT>(x[k], f);
     octet_get<DT>(y, p);
     OctetTurn t;
     rope_load(a.rope, at, o, t);
     rope_turn(a.rope, o, t, f, p);
-    x[k] = octet_put<DT>(f);
+    const Octet<DT> r = octet_put<DT>(f);
+    if (octet_bad<DT>(r)) flags |= octet_bad<DT>(x[k]) || octet_bad<DT>(y) ? KVQ_DEV_NONFINITE : KVQ_DEV_RANGE;
+    x[k] = r;
   }
 }
 

@@ -272,3 +272,34 @@ def test_read_of_one_side_raises_what_both_raise(side, long):
     both = kvq.read_paged(*args)
     i = "kv".index(side)
     assert got[1 - i] is None and torch.equal(got[i], both[i])
+
+
+# ---- keys turned beyond their type ----------------------------------------------------------------------
+@pytest.mark.parametrize("dt,x", [(F16, 60000.0), (BF16, 3e38), (F32, 3e38)])
+@pytest.mark.parametrize("n", [1, 100, 256])
+@pytest.mark.parametrize("inter", [False, True])
+def test_keys_turned_beyond_their_type_are_flagged(dt, x, n, inter):
+    # cos + sin reaches sqrt 2: a pair of large channels leaves the source type
+    rng = np.random.default_rng(85)
+    k, v = normal(rng, (n, 2, 128), dt), normal(rng, (n, 2, 128), dt)
+    pair = (0, 1) if inter else (0, 64)
+    k[n - 1, 1, list(pair)] = synth.to_dtype_values(np.full(2, x, np.float32), dt)
+    p = Paged(fmt(n_sink=0, src_dtype=dt), 2, 1, 3, seed=5)
+    table = torch.ones(n, 128, device="cuda") * np.float32(np.sqrt(0.5))
+    out = ints([0]), ints([0])
+    call = lambda k, rope: kvq.append_paged(p.fmt, p.gpu, ints([0, n]), n, ints([0]), ints([0]), dev(k, dt), dev(v, dt), *out,
+                                            rope=rope, status=p.status)
+    rope = kvq.Rope(table, inter)
+    call(k, rope)
+    assert int(p.status) == RANGE
+    # unturned it fits the type; a number that is none is still called that, turned or not
+    p.status.zero_()
+    if n < 128:
+        call(k, None)
+        assert int(p.status) == 0
+    for bad in (float("nan"), float("inf")):
+        k[n - 1, 1, pair[1]] = bad
+        for r in (rope, None):
+            p.status.zero_()
+            call(k, r)
+            assert int(p.status) & NONFINITE and (n == 256 or int(p.status) == NONFINITE)
