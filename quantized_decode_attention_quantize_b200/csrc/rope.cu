@@ -117,10 +117,11 @@ __global__ void __launch_bounds__(256, 4) norm_rope_kernel(const __grid_constant
     for (int m = 1; m < LPR; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
     if (S.weight) {   // alike over the lanes of a row; rows of one warp may differ
       float eps = a.eps, r = fmaf(ss, a.inv_d, eps);
-      // Squares outside fp32's range: the row is taken 2^70 times smaller or larger, eps by the square of it.
+      // Squares outside fp32's range: the row is taken 2^70 times smaller or 2^100 times larger (below 2^-41 all of
+      // it then, up to 2^59 and down to the smallest subnormal's 2^-49), eps by the square of that.
       const bool big = !(ss <= 0x1p126f), small = r < 0x1p-90f;
       if (big || small) {
-        const float by = big ? 0x1p-70f : 0x1p70f;
+        const float by = big ? 0x1p-70f : 0x1p100f;
         eps *= by;
         eps *= by;
         ss = 0.0f;

@@ -303,3 +303,21 @@ def test_keys_turned_beyond_their_type_are_flagged(dt, x, n, inter):
             p.status.zero_()
             call(k, r)
             assert int(p.status) & NONFINITE and (n == 256 or int(p.status) == NONFINITE)
+
+
+# ---- norm of subnormal rows ---------------------------------------------------------------------------------
+@pytest.mark.parametrize("D", [48, 128, 256])
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("eps", [0.0, 2.0 ** -149, 1e-30])
+def test_norm_of_subnormal_rows(D, dt, eps):
+    # whole numbers of the type's smallest steps (2^-149, bf16 2^-133), exact in every type
+    rng = np.random.default_rng(D + dt)
+    x = rng.integers(-3, 4, (5, 3, D)).astype(np.float32) * np.float32(2.0 ** -149 if dt == F32 else 2.0 ** -133)
+    x[2] *= np.float32(64)
+    x[3] *= np.float32(2.0 ** 60)
+    x[:, :, 0] = x[:, :, 0] + (x[:, :, 0] == 0) * np.abs(x[:, :, 1:]).max(-1)   # no row is all zero
+    w = normal(rng, (D,), dt)
+    st = status0()
+    q, _ = kvq.norm_rope(dev(x, dt), q_weight=dev(w, dt), eps=eps, status=st)
+    check_norm(q, x, w, np.float64(np.float32(eps)), 0.0, None, False, dt)
+    assert int(st) == 0
