@@ -559,7 +559,7 @@ kvq_status kvq_norm_rope(int32_t head_dim, int32_t dtype, int64_t n_tokens, cons
  * first, group j into block block_table[s][t_quant[s] / group_tokens + j], and the rest
  * (fewer than group_tokens, new tokens all) become window rows [0, ...): the flush of the
  * full recent window of [MIX] Figure 4.  t_quant_out / t_res_out (device int32
- * [num_seqs], distinct from the inputs) receive the lengths after it.
+ * [num_seqs], sharing no place with each other or the inputs) receive the lengths after it.
  * rope (nullable) turns the new keys on the way at their positions, or at positions[row]
  * when `positions` (device int32 [n_rows]) is given; the turned key is rounded to
  * src_dtype before it is stored or packed, so a token is packed from the same bits whether

@@ -16,6 +16,12 @@ kvq_status launched(cudaError_t e) { return e == cudaSuccess ? KVQ_OK : KVQ_ERR_
 // A device array of int32 that must be there.
 bool ints(const void* p) { return p && aligned(p, 4); }
 
+// Two arrays of n int32 that share a place.
+bool overlap(const int32_t* p, const int32_t* q, int64_t n) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return (a < b ? b - a : a - b) < (uintptr_t)n * 4;
+}
+
 kvq_status rope_args(const kvq_rope* r, int D, RopeArgs* out) {
   out->table = nullptr;
   out->n_pos = 0;
@@ -167,8 +173,11 @@ kvq_status kvq_append_paged(const kvq_format* f, const kvq_paged_cache* pc, cons
   s = rope_args(rope, a.L.D, &a.rope);
   if (s != KVQ_OK) return s;
   if (positions && !aligned(positions, 4)) return KVQ_ERR_INVALID;
-  if (!ints(tq_out) || !ints(tr_out) || tq_out == tr_out || tq_out == t_quant || tq_out == t_res ||
-      tr_out == t_quant || tr_out == t_res)
+  if (!ints(tq_out) || !ints(tr_out)) return KVQ_ERR_INVALID;
+  // other CTAs still read the lengths when the first ones write theirs
+  const int64_t seqs = pc->num_seqs;
+  if (overlap(tq_out, tr_out, seqs) || overlap(tq_out, t_quant, seqs) || overlap(tq_out, t_res, seqs) ||
+      overlap(tr_out, t_quant, seqs) || overlap(tr_out, t_res, seqs))
     return KVQ_ERR_INVALID;
   const int64_t eb = dtype_bytes(a.L.src_dtype);
   if (!row_strides(k_st, k_sh, eb) || !row_strides(v_st, v_sh, eb)) return KVQ_ERR_INVALID;
