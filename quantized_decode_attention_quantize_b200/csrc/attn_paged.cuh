@@ -267,8 +267,62 @@ constexpr uint32_t kFifteen2 = 0x4B804B80u, kThree2 = 0x42004200u;   // the larg
 // The expansions below form c s + z in fp16.  A scale and a zero-point that fit fp16 can still give numbers beyond
 // it (bf16 and fp32 sources, and fp16 ones that span all of it: 3 s + z = 65536), and an infinity would reach every
 // row of the tile, a weight of 0 included.  The numbers of a channel or token lie between z and c s + z of the
-// largest code, so that one tells whether all are finite.  Where it is not, what has an infinity or NaN in its
-// metadata counts as zero, other numbers beyond fp16 as its largest one, and KVQ_DEV_RANGE is raised.
+// largest code, so that one tells whether all are finite.  A thread that finds one which is not writes its part
+// again by the capped form, which counts what has an infinity or NaN in its metadata as zero and other numbers beyond
+// fp16 as its largest one, and raises KVQ_DEV_RANGE.  The capped forms stand apart, behind the usual stores: within
+// them they cost the usual tiles more (128 rows of 8 sequences over 16384: 218 us, against 193 without any check).
+static __device__ __noinline__ void put_keys_capped(const void* codes, const void* scale, const void* zero, uint32_t slot,
+                                                    int t) {
+  const int o = t & 15, r = t >> 4;
+  const uint4 s = reinterpret_cast<const uint4*>(scale)[o], z = reinterpret_cast<const uint4*>(zero)[o];
+  uint32_t sp[4] = {lo2(s.x, s.z), hi2(s.x, s.z), lo2(s.y, s.w), hi2(s.y, s.w)};
+  uint32_t zp[4] = {lo2(z.x, z.z), hi2(z.x, z.z), lo2(z.y, z.w), hi2(z.y, z.w)};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t m = finite2(sp[k]) & finite2(zp[k]);
+    sp[k] &= m;
+    zp[k] &= m;
+  }
+#pragma unroll 1
+  for (int j = 0; j < 16; ++j) {
+    const uint32_t w = reinterpret_cast<const uint32_t*>(codes)[t + 128 * j];
+    uint32_t x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = cap2(code2<0x000F000Fu, 0x64006400u>(w >> (4 * k), sp[k], zp[k]));
+    st16(slot + (o >> 3) * 16384 + (r + 8 * j) * 128 + (((o & 7) ^ r) << 4), x[0], x[1], x[2], x[3]);
+  }
+}
+// All ones in the halves of token pair `pair` that lie before token `valid`.
+__device__ __forceinline__ uint32_t tokens2(int pair, int valid) {
+  const int left = valid - 2 * pair;
+  return left >= 2 ? 0xffffffffu : left == 1 ? 0x0000ffffu : 0u;
+}
+static __device__ __noinline__ void put_values_capped(const void* codes, const void* scale, const void* zero, uint32_t slot,
+                                                      int t, int valid) {
+  const int W = t & 15;
+#pragma unroll 1
+  for (int half = 0; half < 2; ++half) {
+    const int o = (t >> 4) + 8 * half;
+    uint32_t s[4], z[4], w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      w[j] = reinterpret_cast<const uint32_t*>(codes)[64 * o + 16 * j + W];
+      s[j] = reinterpret_cast<const uint32_t*>(scale)[4 * o + j];
+      z[j] = reinterpret_cast<const uint32_t*>(zero)[4 * o + j];
+      const uint32_t m = tokens2(4 * o + j, valid) & finite2(s[j]) & finite2(z[j]);
+      s[j] &= m;
+      z[j] &= m;
+    }
+#pragma unroll 1
+    for (int e = 0; e < 8; ++e) {
+      uint32_t x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        x[j] = cap2(code2<0x00030003u, 0x64006400u>(w[j] >> (2 * (e & 3) + 8 * (e >> 2)), s[j], z[j]));
+      st16(slot + half * 16384 + W * 128 + (((t >> 4) ^ (W & 7)) << 4) + 2048 * e, x[0], x[1], x[2], x[3]);
+    }
+  }
+}
 
 // A packed group's keys: thread t of 128 takes octet t % 16 (one word) of tokens t / 16 + 8 j.  The eight
 // lanes of a store phase hold eight octets of one token, whose chunks lie in different banks.
@@ -277,29 +331,18 @@ __device__ __forceinline__ int put_keys(const void* codes, const void* scale, co
   const uint4 s = reinterpret_cast<const uint4*>(scale)[o], z = reinterpret_cast<const uint4*>(zero)[o];
   const uint32_t* w = reinterpret_cast<const uint32_t*>(codes) + t;
   const uint32_t at = slot + (o >> 3) * 16384 + r * 128 + (((o & 7) ^ r) << 4);
-  uint32_t s0 = lo2(s.x, s.z), s1 = hi2(s.x, s.z), s2 = lo2(s.y, s.w), s3 = hi2(s.y, s.w);
-  uint32_t z0 = lo2(z.x, z.z), z1 = hi2(z.x, z.z), z2 = lo2(z.y, z.w), z3 = hi2(z.y, z.w);
+  const uint32_t s0 = lo2(s.x, s.z), s1 = hi2(s.x, s.z), s2 = lo2(s.y, s.w), s3 = hi2(s.y, s.w);
+  const uint32_t z0 = lo2(z.x, z.z), z1 = hi2(z.x, z.z), z2 = lo2(z.y, z.w), z3 = hi2(z.y, z.w);
   const uint32_t fits = finite2(h2fma(kFifteen2, s0, z0)) & finite2(h2fma(kFifteen2, s1, z1)) &
                         finite2(h2fma(kFifteen2, s2, z2)) & finite2(h2fma(kFifteen2, s3, z3));
-  if (fits == 0xffffffffu) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const uint32_t x = w[128 * j], y = x >> 8;
-      st16(at + 1024 * j, code2<0x000F000Fu, 0x64006400u>(x, s0, z0), code2<0x00F000F0u, 0x54005400u>(x, s1, z1),
-           code2<0x000F000Fu, 0x64006400u>(y, s2, z2), code2<0x00F000F0u, 0x54005400u>(y, s3, z3));
-    }
-    return 0;
-  }
-  const uint32_t m0 = finite2(s0) & finite2(z0), m1 = finite2(s1) & finite2(z1);
-  const uint32_t m2 = finite2(s2) & finite2(z2), m3 = finite2(s3) & finite2(z3);
-  s0 &= m0; s1 &= m1; s2 &= m2; s3 &= m3;
-  z0 &= m0; z1 &= m1; z2 &= m2; z3 &= m3;
-#pragma unroll 1
   for (int j = 0; j < 16; ++j) {
     const uint32_t x = w[128 * j], y = x >> 8;
-    st16(at + 1024 * j, cap2(code2<0x000F000Fu, 0x64006400u>(x, s0, z0)), cap2(code2<0x00F000F0u, 0x54005400u>(x, s1, z1)),
-         cap2(code2<0x000F000Fu, 0x64006400u>(y, s2, z2)), cap2(code2<0x00F000F0u, 0x54005400u>(y, s3, z3)));
+    st16(at + 1024 * j, code2<0x000F000Fu, 0x64006400u>(x, s0, z0), code2<0x00F000F0u, 0x54005400u>(x, s1, z1),
+         code2<0x000F000Fu, 0x64006400u>(y, s2, z2), code2<0x00F000F0u, 0x54005400u>(y, s3, z3));
   }
+  if (fits == 0xffffffffu) return 0;
+  put_keys_capped(codes, scale, zero, slot, t);
   return KVQ_DEV_RANGE;
 }
 // A packed group's values: thread t takes word W = t % 16 (eight channels) of the token octets t / 16 and
@@ -307,41 +350,22 @@ __device__ __forceinline__ int put_keys(const void* codes, const void* scale, co
 __device__ __forceinline__ int put_values(const void* codes, const void* scale, const void* zero, uint32_t slot, int t,
                                           int valid) {
   const int W = t & 15;
-  int flags = 0;
+  uint32_t fits = 0xffffffffu;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     const int o = (t >> 4) + 8 * half;
     const uint4 sv = reinterpret_cast<const uint4*>(scale)[o], zv = reinterpret_cast<const uint4*>(zero)[o];
-    uint32_t s[4] = {sv.x, sv.y, sv.z, sv.w}, z[4] = {zv.x, zv.y, zv.z, zv.w}, w[4], fits = 0xffffffffu;
+    uint32_t s[4] = {sv.x, sv.y, sv.z, sv.w}, z[4] = {zv.x, zv.y, zv.z, zv.w}, w[4];
     const uint32_t* c = reinterpret_cast<const uint32_t*>(codes) + 64 * o + W;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       w[j] = c[16 * j];
-      const int left = valid - 8 * o - 2 * j;
-      const uint32_t m = left >= 2 ? 0xffffffffu : left == 1 ? 0x0000ffffu : 0u;
+      const uint32_t m = tokens2(4 * o + j, valid);
       s[j] &= m;
       z[j] &= m;
       fits &= finite2(h2fma(kThree2, s[j], z[j]));
     }
     const uint32_t at = slot + half * 16384 + W * 128 + (((t >> 4) ^ (W & 7)) << 4);
-    if (fits != 0xffffffffu) {
-      flags = KVQ_DEV_RANGE;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t m = finite2(s[j]) & finite2(z[j]);
-        s[j] &= m;
-        z[j] &= m;
-      }
-#pragma unroll 1
-      for (int e = 0; e < 8; ++e) {
-        uint32_t x[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          x[j] = cap2(code2<0x00030003u, 0x64006400u>(w[j] >> (2 * (e & 3) + 8 * (e >> 2)), s[j], z[j]));
-        st16(at + 2048 * e, x[0], x[1], x[2], x[3]);
-      }
-      continue;
-    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       uint32_t x[4];
@@ -356,7 +380,9 @@ __device__ __forceinline__ int put_values(const void* codes, const void* scale, 
       st16(at + 2048 * e, x[0], x[1], x[2], x[3]);
     }
   }
-  return flags;
+  if (fits == 0xffffffffu) return 0;
+  put_values_capped(codes, scale, zero, slot, t, valid);
+  return KVQ_DEV_RANGE;
 }
 
 // Eight channels (octet o) of raw token r of sequence s, head h: the sink's rows, then the window's.
