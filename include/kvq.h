@@ -543,9 +543,10 @@ typedef struct kvq_head_rows {
  *   u = x / sqrt(mean(x^2) + eps) * (weight_offset + weight)      (u = x without a weight)
  *   y = u turned by the table's row of the token's position
  * in fp32, rounded once to `dtype`; squares beyond fp32's range do not matter.  A NaN or
- * Inf raises KVQ_DEV_NONFINITE.  `k` may be NULL (queries only).  rope may be NULL (norm
- * only).  positions: device int32 [n_tokens], NULL for position = token index; a position
- * outside [0, n_pos) leaves the row unturned and raises KVQ_DEV_BOUNDS. */
+ * Inf among the x raises KVQ_DEV_NONFINITE (a y beyond `dtype` is Inf and raises nothing).
+ * `k` may be NULL (queries only).  rope may be NULL (norm only).  positions: device int32
+ * [n_tokens], NULL for position = token index; a position outside [0, n_pos) leaves the row
+ * unturned and raises KVQ_DEV_BOUNDS. */
 kvq_status kvq_norm_rope(int32_t head_dim, int32_t dtype, int64_t n_tokens, const kvq_head_rows* q,
                          const kvq_head_rows* k, float eps, float weight_offset, const kvq_rope* rope,
                          const int32_t* positions, int32_t* d_status, void* stream);
@@ -563,9 +564,11 @@ kvq_status kvq_norm_rope(int32_t head_dim, int32_t dtype, int64_t n_tokens, cons
  * rope (nullable) turns the new keys on the way at their positions, or at positions[row]
  * when `positions` (device int32 [n_rows]) is given; the turned key is rounded to
  * src_dtype before it is stored or packed, so a token is packed from the same bits whether
- * or not it passed through the window.  Where the turn takes a finite key beyond
- * src_dtype (by up to sqrt 2 and the table's amplitude) KVQ_DEV_RANGE is raised.  Packed groups equal kvq_quantize_kv_paged's.
- * max_new: host bound on the new tokens of one sequence.  A sequence is left as it was, its
+ * or not it passed through the window.  Where the turn takes a finite key beyond src_dtype
+ * (by up to sqrt 2 and the table's amplitude) KVQ_DEV_RANGE is raised.  Packed groups equal
+ * kvq_quantize_kv_paged's, also where an element is NaN or Inf or a scale does not fit.
+ * max_new: host bound on the new tokens of one sequence, at most n_rows (so for max_rows and
+ * max_new of the calls below).  A sequence is left as it was, its
  * lengths copied and KVQ_DEV_BOUNDS raised, when its rows or lengths are out of range, it
  * brings more than max_new tokens, t_quant[s] is not a multiple of group_tokens, or a block
  * it needs is missing from the table or outside the pool.  A position outside the rotary
