@@ -23,7 +23,8 @@
  *    the kernels: KVQ_DEV_NONFINITE when an input element is NaN or Inf (the inputs
  *    are rejected, as the INT8 page prescribes: the affected outputs are
  *    unspecified), KVQ_DEV_RANGE when a scale, zero-point or outlier value does not
- *    fit fp16, KVQ_DEV_TIMEOUT when a bounded in-kernel wait expired.  The caller
+ *    fit fp16 (the serving steps say where else), KVQ_DEV_TIMEOUT when a bounded
+ *    in-kernel wait expired.  The caller
  *    zeroes the word and reads it back when it wants to know.
  *  - Layouts.  B = batch, Hkv = KV heads, Hq = query heads, G = Hq / Hkv, D = head
  *    dimension.  Query head h reads KV head h / G (contiguous GQA grouping).

@@ -16,9 +16,9 @@
 // there n = 16, which serves up to fp16's largest scale.  A smaller range of the queries would serve all
 // groups, but costs small scales their last bits: q s / 16 is subnormal below 2^-14.
 //
-// What bounds it: the expansion and the softmax on CUDA cores (about 200 instructions per 16 tokens and warp);
-// the packed bytes pass once per 16 rows.  4 tokens x 8 sequences over 32768 and fewer, 8 x 4 heads: 99 us, of
-// which the tiles take 67 (1250 cycles per 16 tokens and warp, two warps per scheduler at 0.3 instructions a clock).
+// What bounds it: the expansion and the softmax on CUDA cores, 476 warp instructions and 1.5 us per 16 tokens, at
+// two warps per scheduler (255 registers), which use 42 % of the issue slots; the packed bytes pass once per 16
+// rows.  4 tokens and fewer x 8 sequences over 32768 and fewer, 8 x 4 heads: 99 us with the merge.
 #include "attn_paged.cuh"
 
 namespace kvq {

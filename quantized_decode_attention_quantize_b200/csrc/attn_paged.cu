@@ -345,9 +345,9 @@ __device__ __forceinline__ void softmax_warp(const AttnArgs& a, const Work& work
   }
 }
 
-// One CTA per SM, each with its run of units.  3.0 us per pair of a 256-row block and a 128-token tile (its
-// products alone 1.5 at the clock of a long run): softmax (1.9 alone) and expansion (1.1 alone) share the SM's
-// issue slots, which is why the expansion has eight warps and no more.
+// One CTA per SM, each with its run of units.  64 tokens x 8 sequences over 16384, 8 x 4 heads: 261 us, 4.7 us per
+// pair of a 256-row block and a 128-token tile, where the products need 1.5 at the measured bf16 rate: softmax and
+// expansion share the SM's issue slots and its instruction cache, so the expansion has eight warps and no more.
 __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnArgs a,
                                                               const __grid_constant__ Work work) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -473,14 +473,17 @@ cudaError_t launch_merge(const AttnArgs& a, const Work& w, int runs, cudaStream_
 }
 }  // namespace attn
 
-// Expanding the pages first pays from more than one row block (256 rows) per sequence on.  Measured, us, without
-// / with: 64 tokens x 4 heads (one block) over 18k 78 / 113; 13 ragged chunks of 285 rows over 4k, 32 heads
-// 605 / 518; 2048 tokens x 4 heads over 16k 900 / 690 when both were first built.
+// Expanding the pages first pays from more than one row block (256 rows) per sequence on, in batches; a sequence by
+// itself has to bring more than 512 (and fewer than 2048).  Measured, us, without / with, 8 x 4 heads, rows per sequence: 13 sequences of
+// 4096 tokens 256 rows 171 / 190, 384 rows 304 / 256, 2048 rows 908 / 613; 32 sequences of 2048 256 rows 234 / 228,
+// 384 rows 450 / 319; 1 sequence of 18432 256 rows 87 / 116, 512 rows 115 / 134, 2048 rows 281 / 243.
 bool attn_wide_pays(int num_seqs, int G, int64_t n_rows) { return n_rows * G > (int64_t)num_seqs * 256; }
 
-// Blocks of 16 rows, a warp each, up to 64 rows a sequence; blocks of 256 on the whole CTA above.  16 rows (4 tokens
-// x 4 heads) of 8 sequences over 32768 and fewer: 99 us against 225 on the whole CTA; 64 rows 199 (the pages pass
-// four times), 68 to 96 rows on the whole CTA 211 to 222.
+// Blocks of 16 rows, a warp each, up to 64 rows a sequence; blocks of 256 on the whole CTA above.  Measured, us,
+// narrow / whole CTA, 8 x 4 heads: 8 sequences over 32768 and fewer 16 rows 130 / 273, 48 rows 255 / 284, 64 rows
+// 321 / 263; 64 sequences of 4096 16 rows 202 / 507, 48 rows 540 / 517, 64 rows 693 / 488; 1 sequence of 32768 16
+// rows 81 / 89, 64 rows 97 / 87.  These have 64 rows in every sequence (the pages pass four times); in a ragged
+// batch that few reach the sides meet later: 64 rows 199, 68 to 96 rows on the whole CTA 211 to 222.
 constexpr int kNarrowRows = 64, kNarrowWarps = 8;
 bool narrow(int G, int64_t max_new) { return max_new * G <= kNarrowRows; }
 size_t make_work_for(int G, int64_t max_new, void* ws, Work* w, int* runs) {

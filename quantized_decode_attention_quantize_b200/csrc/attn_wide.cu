@@ -25,7 +25,7 @@ constexpr size_t kExpandSmem = 2 * kTile;
 
 // CTAs take (tile, head) in turn over all sequences that have query rows; threads 0-127 keys, the others
 // values, both into shared memory, from where one bulk copy writes the 64 KB out.  Three CTAs per SM (shared
-// memory) hide one another's loads; 13 sequences of 4096 tokens and fewer, 32 heads: about 110 us, bound by the
+// memory) hide one another's loads; 13 sequences of 4096 tokens and fewer, 32 heads: 126 us, bound by the
 // dependent loads of a tile (page, codes) and the 64 KB stored for each 13 KB read.
 __global__ void __launch_bounds__(kExpandThreads, 3) expand_kernel(const __grid_constant__ AttnArgs a, char* tiles,
                                                                    int64_t bound) {
@@ -327,9 +327,8 @@ __device__ __forceinline__ void softmax_warp(const AttnArgs& a, const Work& work
   }
 }
 
-// 2.2 us per pair of a 256-row block and a 128-token tile, of which products and copies alone take 1.86 (64 KB
-// per pair from L2 are 10 TB/s over all SMs); 2048 tokens x 8 x 4 heads over 16384: 683 us with the expansion,
-// 855 TFLOP/s.
+// 2048 tokens x 8 x 4 heads over 16384: 675 us with the expansion and the merge, 865 TFLOP/s; 2.7 us per pair of a
+// 256-row block and a 128-token tile (64 KB per pair through L2), the tensor pipe busy for 45 % of the time.
 __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_constant__ AttnArgs a,
                                                                 const __grid_constant__ Work work, const char* tiles,
                                                                 int64_t bound) {

@@ -203,8 +203,10 @@ __device__ __forceinline__ void turn_rows(const AppendArgs& a, int which, int o,
 // the two row slices of a warp, then over the 8 warps in shared memory; values: a token's over its 16
 // lanes.  The rows of a value pair sit in one thread, which owns the pair's word.
 // Rows kept as loaded leave three CTAs per SM (80 registers) where fp32 registers left one: a batch of prompts,
-// 30k tokens of 8 heads in bf16, 310 us with one CTA, 129 with two, 116 with three (1.2 TB/s of rows in and
-// codes out; bound by the chain of dependent loads and barriers of a unit, and by its arithmetic).
+// 30k tokens of 8 heads in bf16, 310 us with one CTA, 129 with two, 117 with three (1.2 TB/s of rows in and
+// codes out; bound by instruction fetch, the chain of dependent loads and barriers of a unit, and its
+// arithmetic).  fp32 rows and transformed keys need 178 to 192 registers and have one CTA: 227 and 254 us against 135
+// of bf16 in the same run with its caches flushed.
 template <int DT, bool ROT>
 __global__ void __launch_bounds__(kThreads, DT == KVQ_F32 || ROT ? 1 : 3)
     append_paged_kernel(const __grid_constant__ AppendArgs a) {
