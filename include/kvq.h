@@ -24,8 +24,8 @@
  *    are rejected, as the INT8 page prescribes: the affected outputs are
  *    unspecified), KVQ_DEV_RANGE when a scale, zero-point or outlier value does not
  *    fit fp16 (the serving steps say where else), KVQ_DEV_TIMEOUT when a bounded
- *    in-kernel wait expired.  The caller
- *    zeroes the word and reads it back when it wants to know.
+ *    in-kernel wait expired.  The caller zeroes the word and reads it back when it
+ *    wants to know.
  *  - Layouts.  B = batch, Hkv = KV heads, Hq = query heads, G = Hq / Hkv, D = head
  *    dimension.  Query head h reads KV head h / G (contiguous GQA grouping).
  *    Every cache array is [B][Hkv][slab] with the per-(b, kv-head) slab laid out as
@@ -596,10 +596,11 @@ kvq_status kvq_read_paged(const kvq_format* fmt, const kvq_paged_cache* cache, c
                           int32_t* d_status, void* stream);
 
 /* Workspace bytes for kvq_attention_paged with these sizes (depends on the current
- * device's SM count); 0 for sizes it refuses.  For long chunks (more than 256 query rows
- * per KV head and sequence on average) it includes room for the pages expanded to fp16, 64 KB per
- * page of each sequence's bound and KV head, where that is at most 4 GiB; a smaller
- * workspace, down to what the call needs for other sizes, runs too, more slowly. */
+ * device's SM count); 0 for sizes it refuses.  Enough for a smaller max_new, too.  For long
+ * chunks (more than 256 query rows per KV head and sequence on average) it includes room for
+ * the pages expanded to fp16, 64 KB per page of each sequence's bound and KV head, where that
+ * is at most 4 GiB; a smaller workspace, down to what the call needs for other sizes, runs
+ * too, more slowly.  Calls that may run at the same time need a workspace each. */
 size_t kvq_attention_paged_workspace_bytes(const kvq_format* fmt, int32_t num_seqs, int32_t q_heads,
                                            int32_t kv_heads, int64_t n_rows, int64_t max_new,
                                            int64_t max_t_quant, int32_t max_t_res);
@@ -610,6 +611,7 @@ size_t kvq_attention_paged_workspace_bytes(const kvq_format* fmt, int32_t num_se
  * t_quant[s] + t_res[s] tokens; row i attends to the tokens at positions j <= L - n + i
  * when causal, to all L otherwise:
  *   out[i][h] = sum_j softmax_j(softmax_scale * q[i][h] . k^_j) v^_j
+ * (the scaled products have to stay within fp32's range).
  * out: device [n_rows][q_heads][D] in out_dtype; lse (device fp32 [n_rows][q_heads], may
  * be NULL): the natural log of the softmax denominator, as kvq_merge_states takes it.  A row
  * that sees no token (n > L) gets out = 0 and lse = -inf.  The products run on the tensor

@@ -236,7 +236,7 @@ static kvq_status attn_sizes(const kvq_format* f, int32_t num_seqs, int32_t Hq, 
 size_t kvq_attention_paged_workspace_bytes(const kvq_format* f, int32_t num_seqs, int32_t Hq, int32_t Hkv,
                                            int64_t n_rows, int64_t max_new, int64_t max_tq, int32_t max_tr) {
   if (attn_sizes(f, num_seqs, Hq, Hkv, n_rows, max_new, max_tq, max_tr) != KVQ_OK) return 0;
-  size_t n = attn_paged_workspace(Hq / Hkv, max_new);
+  size_t n = attn_paged_workspace_upto(Hq / Hkv, max_new);
   if (attn_wide_pays(num_seqs, Hq / Hkv, n_rows)) {
     const size_t tiles = attn_wide_tiles(num_seqs, Hkv, max_tq, max_tr, f->n_sink);
     if (tiles <= kMaxTiles) n += tiles;

@@ -497,6 +497,12 @@ size_t attn_paged_workspace(int G, int64_t max_new) {
   return make_work_for(G, max_new, nullptr, &w, &runs);
 }
 
+size_t attn_paged_workspace_upto(int G, int64_t max_new) {   // the narrow kernel has more runs, and slots
+  const int64_t few = max_new < kNarrowRows / G ? max_new : kNarrowRows / G;
+  const size_t a = attn_paged_workspace(G, max_new), b = attn_paged_workspace(G, few);
+  return a > b ? a : b;
+}
+
 cudaError_t launch_attn_paged(const AttnArgs& args, cudaStream_t s) {
   AttnArgs a = args;
   int runs;

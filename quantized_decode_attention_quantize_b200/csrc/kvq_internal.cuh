@@ -214,8 +214,10 @@ struct AttnArgs {
   const void* res[2];
   int32_t* status;
 };
-// The bytes the call cannot do without, and those of the expanded pages where they pay.
+// The bytes the call cannot do without, those that serve every smaller max_new as well, and those of the expanded
+// pages where they pay.
 size_t attn_paged_workspace(int G, int64_t max_new);
+size_t attn_paged_workspace_upto(int G, int64_t max_new);
 bool attn_wide_pays(int num_seqs, int G, int64_t n_rows);
 size_t attn_wide_tiles(int num_seqs, int Hkv, int64_t max_t_quant, int max_t_res, int n_sink);
 cudaError_t launch_attn_paged(const AttnArgs& a, cudaStream_t s);
