@@ -562,9 +562,18 @@ _HEAD_ROWS = struct.Struct("@PPqqqqiP")   # kvq_head_rows
 assert _HEAD_ROWS.size == ctypes.sizeof(kvq_head_rows)
 
 
+def _row_strides(x):
+    """Strides of rows x [T, H, D]; where a dimension has no extent, those of a contiguous tensor."""
+    t, h, c = x.stride()
+    T, H, D = x.shape
+    if H > 1 and T > 1:
+        return t, h, c
+    return (t if T > 1 else H * D), (h if H > 1 and T else D), (c if T else 1)
+
+
 def _head_rows(x, y, weight, what):
-    xt, xh, xc = x.stride()
-    yt, yh, yc = y.stride()
+    xt, xh, xc = _row_strides(x)
+    yt, yh, yc = _row_strides(y) if y.dim() == 3 else (0, 0, 0)
     if xc != 1 or yc != 1 or y.shape != x.shape or y.dtype != x.dtype or y.device != x.device:
         raise ValueError(f"{what}: channels must be contiguous, the output of the same shape, dtype and device")
     w = 0
@@ -617,8 +626,8 @@ def append_paged(fmt, cache: PagedCache, cu_new: torch.Tensor, max_new: int, t_q
     dt, d = TORCH_DTYPE[fmt.src_dtype], cache.device
     rows = k_src.shape[0]
     shape = (rows, cache.H, fmt.head_dim)
-    kt, kh, kc = k_src.stride() if k_src.dim() == 3 else (0, 0, 0)
-    vt, vh, vc = v_src.stride() if v_src.dim() == 3 else (0, 0, 0)
+    kt, kh, kc = _row_strides(k_src) if k_src.dim() == 3 else (0, 0, 0)
+    vt, vh, vc = _row_strides(v_src) if v_src.dim() == 3 else (0, 0, 0)
     if k_src.shape != shape or v_src.shape != shape or k_src.dtype != dt or v_src.dtype != dt or kc != 1 or vc != 1 or \
             k_src.device != d or v_src.device != d:
         raise ValueError("k_src, v_src: [rows, kv_heads, head_dim] in the format's source dtype is needed")
